@@ -368,6 +368,121 @@ int nomas_w8a16_linear(const void *x, int64_t m, int64_t k_in, int64_t ldx, cons
 /* Synchronise `stream`, read and clear a linear layer's device error word. */
 int nomas_status_read(int32_t *status, nomas_stream stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Rotary positions with several axes (time, height, width), applied to the queries and keys of video
+ * and text tokens before nomas_kv_append / nomas_attn_prepare / nomas_attn_run (the pages name the
+ * latent grid, papers.ananclaw.com 这是什么, and no formula; the definition is the common one):
+ *   the head's channels are cut, from channel 0, into axis_dim[0] time channels, axis_dim[1] height and
+ *   axis_dim[2] width channels; channels behind them pass through bit for bit;
+ *   pair i (0 <= i < axis_dim[a] / 2) of axis a is channels (2i, 2i + 1) of the axis
+ *   (NOMAS_ROPE_INTERLEAVED) or (i, i + axis_dim[a] / 2) (NOMAS_ROPE_HALVES), and turns by
+ *   p_a * theta^(-2 i / axis_dim[a]) for a token at position p_a:
+ *       y1 = x1 cos - x2 sin,   y2 = x1 sin + x2 cos
+ *   inverse != 0 turns by the negative angle: the inverse, and the gradient with respect to x of a
+ *   gradient with respect to y (a rotation's adjoint is its inverse).
+ * Angles are reduced in fp64, sines and products are fp32, the result is rounded once to the type.
+ * ------------------------------------------------------------------------------------------ */
+#define NOMAS_ROPE_INTERLEAVED 0
+#define NOMAS_ROPE_HALVES 1
+#define NOMAS_ROPE_MAX_TENSORS 4
+#define NOMAS_ROPE_MAX_HEAD_DIM 256
+
+typedef struct {
+    int32_t head_dim;          /* D, a multiple of 8, at most NOMAS_ROPE_MAX_HEAD_DIM */
+    int32_t axis_dim[3];       /* channels of time, height, width: even, >= 0, 2 <= sum <= D */
+    int32_t pairing;           /* NOMAS_ROPE_INTERLEAVED or NOMAS_ROPE_HALVES */
+    int32_t _pad;
+    double theta;              /* base, finite and > 0 */
+} nomas_rope_spec;
+
+/* Positions of video tokens in memory order: token n is frame n / (grid_h grid_w), row, column of the
+ * latent grid, at position origin[a] + step[a] * index on each axis. */
+typedef struct {
+    double origin[3], step[3]; /* time, height, width; finite */
+    int32_t grid_h, grid_w;    /* >= 1, grid_h * grid_w < 2^31 */
+} nomas_rope_grid;
+
+/* One tensor of a call: [tokens][heads][head_dim], strides in elements, multiples of 8 (0 allowed for x: a
+ * value that several tokens or heads share).  y may be x with the same strides (in place); otherwise x and
+ * y, and the tensors of one call, must not overlap. */
+typedef struct {
+    const void *x;
+    void *y;
+    int64_t x_tok_stride, x_head_stride, y_tok_stride, y_head_stride;
+    int32_t heads;             /* >= 1 */
+    int32_t _pad;
+} nomas_rope_tensor;
+
+/* Rotate n_tensors (1 .. NOMAS_ROPE_MAX_TENSORS) tensors of the same tokens in one launch, e.g. q and k.
+ *   grid       positions from the latent grid, or NULL
+ *   positions  fp32 [tokens][3] (device): time, height, width of each token; exactly one
+ *              of grid and positions is given.  A non-finite position gives NaN in its axis' channels.
+ *   dtype      NOMAS_DTYPE_BF16 or NOMAS_DTYPE_F32, of every x and y
+ * tokens = 0 does nothing.  Runs on the device that holds the first tensor.  Errors: NOMAS_EINVAL for a
+ * bad pointer, stride, spec or grid; NOMAS_EUNSUPPORTED for 2^31 tokens or more. */
+int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *grid, const float *positions, int64_t tokens,
+               const nomas_rope_tensor *tensors, int n_tensors, int dtype, int inverse, nomas_stream stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Layer norm over the rows of x [rows][cols], with one weight and bias row per group of rows: the norm
+ * and modulation in front of the DiT's linear layers (rows_per_group = the tokens of a latent frame for
+ * a modulation per frame), or a learned layer norm (rows_per_group = 0: one group).
+ *   mean = sum x / cols,  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),  xhat = (x - mean) rstd
+ *   y = xhat (u + w) + b      u = 1 with unit_offset != 0 (w is a scale around one), else 0
+ * Backward, with g = dy (u + w):
+ *   dx = rstd (g - mean(g) - xhat mean(g xhat)),   dw = sum dy xhat,  db = sum dy over a group's rows
+ * Row r belongs to group r / rows_per_group; there are ceil(rows / rows_per_group) groups (1 if 0).
+ * Statistics, sums and products are fp32; y and dx are rounded once.  The sums of dw and db run in a
+ * fixed order (no atomics): the same call gives the same bits.
+ * x, dx are x_dtype, y, dy are y_dtype, w and b are p_dtype (each NOMAS_DTYPE_F32 or _BF16); pitches in
+ * elements, >= cols.  cols <= NOMAS_NORM_MAX_COLS, any value; 16-byte aligned pointers with cols and
+ * pitches that are multiples of 8 take wide loads, every other layout (element aligned) narrow ones.
+ * rows = 0 writes no y, mean, rstd or dx (dw and db become 0 when rows_per_group is 0).
+ * Runs on the device that holds x.  Errors: NOMAS_EINVAL, NOMAS_EUNSUPPORTED (cols, rows >= 2^31). */
+#define NOMAS_NORM_MAX_COLS 16384
+
+/* w, b nullable (y = xhat without w and b, unit_offset then without effect); mean, rstd fp32 [rows], nullable.
+ * y may be x when the types and pitches agree. */
+int nomas_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int64_t ldx, int x_dtype, const void *w,
+                        const void *b, int64_t ldp, int p_dtype, int64_t rows_per_group, int unit_offset, float eps,
+                        void *y, int64_t ldy, int y_dtype, float *mean, float *rstd, nomas_stream stream);
+
+/* Bytes of the backward pass' workspace: 0 on invalid arguments, else at least 16. */
+size_t nomas_layernorm_workspace_bytes(int64_t rows, int64_t cols, int64_t rows_per_group);
+
+/* mean, rstd: of the forward call.  dx, dw, db: each nullable, not all; dw, db fp32 [groups][cols], pitch
+ * ldg.  dx may be dy or x when types and pitches agree.  workspace: device buffer, 16-byte aligned, read
+ * and written by this call alone (calls that share it must not overlap); NULL allowed without dw and db. */
+int nomas_layernorm_bwd(const void *dy, int64_t lddy, int y_dtype, const void *x, int64_t ldx, int x_dtype,
+                        int64_t rows, int64_t cols, const void *w, int64_t ldp, int p_dtype, int64_t rows_per_group,
+                        int unit_offset, const float *mean, const float *rstd, void *dx, int64_t lddx, float *dw,
+                        float *db, int64_t ldg, void *workspace, nomas_stream stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Linear layer with 4-bit weights and group scales (the INT8 layer above at half the bytes, for the
+ * products of a few rows that read every weight once: modulation vectors, timestep embeddings, single
+ * tokens).  Layout of W [N][K]: codes uint8 [N][K / 2], column k of a row in byte k / 2, even columns in
+ * the low half, stored as code + 8 with codes in -8 .. 7; scales bf16 [N][ceil(K / group)], group 32, 64 or
+ * 128 consecutive columns (the last one may be short); K a multiple of 32.
+ *   weight  w_nk = bf16(code * scale)         output  y = x W^T, bf16 x, fp32 sums, y fp32 or bf16
+ * Pointers 16-byte aligned, ldx a multiple of 8, ldy >= N.  m = 0 does nothing. */
+
+/* Quantise bf16 weights w [N][K] (pitch ldw): per group s = bf16(RN(absmax / 7)), code = clamp(rint(w / s),
+ * -7, 7) (fp32 division, half-even); s = 0 gives codes 0; a group with a non-finite weight gets s = NaN. */
+int nomas_w4_quantize(const void *w, int64_t n_out, int64_t k_in, int64_t ldw, int group, uint8_t *codes, void *scales,
+                      nomas_stream stream);
+/* Dequantise into bf16 weights w [N][K] (dense). */
+int nomas_w4_dequant(const uint8_t *codes, const void *scales, int group, int64_t n_out, int64_t k_in, void *w,
+                     nomas_stream stream);
+/* Bytes of the workspace of a nomas_w4a16_linear call with m rows: 0 for few rows (the weights are widened
+ * in registers), else N * K * 2 for the transient bf16 weights of the tensor-core GEMM. */
+size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in);
+/* y [M][N] = x [M][K] W^T.  workspace may be NULL when nomas_w4a16_workspace_bytes gives 0; status as for
+ * nomas_linear_bf16.  Runs on the device that holds the codes. */
+int nomas_w4a16_linear(const void *x, int64_t m, int64_t k_in, int64_t ldx, const uint8_t *codes, const void *scales,
+                       int group, int64_t n_out, void *y, int64_t ldy, int y_dtype, void *workspace, int32_t *status,
+                       nomas_stream stream);
+
 /* Synchronise `stream`, read and clear the device error word.  Returns NOMAS_OK
  * or the first device-side error recorded since the last call. */
 int nomas_device_status(const nomas_kv_cache *cache, nomas_stream stream);

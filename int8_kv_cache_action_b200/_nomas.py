@@ -25,6 +25,10 @@ NOMAS_STATIC_POOL_FLOATS = 2 << 20
 NOMAS_MAX_SPARSE_CANDIDATES = 8192
 NOMAS_MAX_SELECT_FRAMES = 64
 NOMAS_DTYPE_F32, NOMAS_DTYPE_BF16 = 0, 1
+NOMAS_ROPE_INTERLEAVED, NOMAS_ROPE_HALVES = 0, 1
+NOMAS_ROPE_MAX_TENSORS = 4
+NOMAS_ROPE_MAX_HEAD_DIM = 256
+NOMAS_NORM_MAX_COLS = 16384
 
 EXPORTED = ["nomas_kv_cache_bytes", "nomas_kv_cache_init", "nomas_kv_cache_destroy", "nomas_kv_cache_state",
             "nomas_kv_append", "nomas_mask_layout_query", "nomas_mask_bytes", "nomas_mask_build",
@@ -33,7 +37,9 @@ EXPORTED = ["nomas_kv_cache_bytes", "nomas_kv_cache_init", "nomas_kv_cache_destr
             "nomas_set_wait_limit_ns", "nomas_set_text_split", "nomas_set_attn_kernel", "nomas_attn_prepare", "nomas_attn_run", "nomas_kv_frame_record_bytes",
             "nomas_kv_retained", "nomas_kv_evicted_by", "nomas_kv_archive", "nomas_kv_select",
             "nomas_w8_quantize", "nomas_w8_dequant", "nomas_linear_bf16", "nomas_w8a16_workspace_bytes",
-            "nomas_w8a16_linear", "nomas_status_read"]
+            "nomas_w8a16_linear", "nomas_status_read", "nomas_rope", "nomas_layernorm_fwd",
+            "nomas_layernorm_workspace_bytes", "nomas_layernorm_bwd", "nomas_w4_quantize", "nomas_w4_dequant",
+            "nomas_w4a16_workspace_bytes", "nomas_w4a16_linear"]
 
 
 class nomas_cache_dims(ctypes.Structure):
@@ -64,6 +70,22 @@ class nomas_mask_layout(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ["history_tokens", "head_tokens", "n_query", "text_tokens"]] + \
                [(n, ctypes.c_size_t) for n in ["off_class", "off_sel", "off_score", "off_qmean", "off_kmean",
                                                 "off_txtwin", "off_count", "off_list", "total_bytes"]]
+
+
+class nomas_rope_spec(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("axis_dim", ctypes.c_int32 * 3), ("pairing", ctypes.c_int32),
+                ("_pad", ctypes.c_int32), ("theta", ctypes.c_double)]
+
+
+class nomas_rope_grid(ctypes.Structure):
+    _fields_ = [("origin", ctypes.c_double * 3), ("step", ctypes.c_double * 3), ("grid_h", ctypes.c_int32),
+                ("grid_w", ctypes.c_int32)]
+
+
+class nomas_rope_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_tok_stride", ctypes.c_int64),
+                ("x_head_stride", ctypes.c_int64), ("y_tok_stride", ctypes.c_int64),
+                ("y_head_stride", ctypes.c_int64), ("heads", ctypes.c_int32), ("_pad", ctypes.c_int32)]
 
 
 _p = ctypes.c_void_p
@@ -108,6 +130,18 @@ _sigs = {
     "nomas_w8a16_linear": (ctypes.c_int, [_p, _i64, _i64, _i64, _p, _p, _i64, _p, _i64, ctypes.c_int, _p, _p,
                                           _p]),
     "nomas_status_read": (ctypes.c_int, [_p, _p]),
+    "nomas_rope": (ctypes.c_int, [ctypes.POINTER(nomas_rope_spec), ctypes.POINTER(nomas_rope_grid), _p, _i64,
+                                  ctypes.POINTER(nomas_rope_tensor), ctypes.c_int, ctypes.c_int, ctypes.c_int, _p]),
+    "nomas_layernorm_fwd": (ctypes.c_int, [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p, _i64, ctypes.c_int, _i64,
+                                           ctypes.c_int, _f32, _p, _i64, ctypes.c_int, _p, _p, _p]),
+    "nomas_layernorm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "nomas_layernorm_bwd": (ctypes.c_int, [_p, _i64, ctypes.c_int, _p, _i64, ctypes.c_int, _i64, _i64, _p, _i64,
+                                           ctypes.c_int, _i64, ctypes.c_int, _p, _p, _p, _i64, _p, _p, _i64, _p, _p]),
+    "nomas_w4_quantize": (ctypes.c_int, [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p, _p]),
+    "nomas_w4_dequant": (ctypes.c_int, [_p, _p, ctypes.c_int, _i64, _i64, _p, _p]),
+    "nomas_w4a16_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "nomas_w4a16_linear": (ctypes.c_int, [_p, _i64, _i64, _i64, _p, _p, ctypes.c_int, _i64, _p, _i64, ctypes.c_int,
+                                          _p, _p, _p]),
 }
 for _name, (_res, _args) in _sigs.items():
     _f = getattr(lib, _name)
@@ -303,3 +337,59 @@ def nomas_w8a16_linear(x, m, k_in, ldx, codes, scales, n_out, y, ldy, y_dtype, w
 
 def nomas_status_read(status, stream=0):
     return lib.nomas_status_read(status, stream or None)
+
+
+# ------------------------------------------------------------------------------------------------
+# rotary positions, layer norm, 4-bit-weight linear layer
+# ------------------------------------------------------------------------------------------------
+
+def make_rope_spec(head_dim, axis_dims, theta=10000.0, pairing=NOMAS_ROPE_INTERLEAVED):
+    return nomas_rope_spec(head_dim, (ctypes.c_int32 * 3)(*axis_dims), pairing, 0, theta)
+
+
+def make_rope_grid(grid_h, grid_w, origin=(0.0, 0.0, 0.0), step=(1.0, 1.0, 1.0)):
+    return nomas_rope_grid((ctypes.c_double * 3)(*origin), (ctypes.c_double * 3)(*step), grid_h, grid_w)
+
+
+def make_rope_tensors(tensors):
+    """tensors: (x, y, x_tok_stride, x_head_stride, y_tok_stride, y_head_stride, heads) each."""
+    return (nomas_rope_tensor * max(1, len(tensors)))(*[nomas_rope_tensor(*t, 0) for t in tensors])
+
+
+def nomas_rope(spec, grid, positions, tokens, tensors, n_tensors, dtype, inverse, stream=0):
+    return lib.nomas_rope(ctypes.byref(spec), ctypes.byref(grid) if grid is not None else None, positions or None,
+                          tokens, tensors, n_tensors, dtype, int(inverse), stream or None)
+
+
+def nomas_layernorm_fwd(x, rows, cols, ldx, x_dtype, w, b, ldp, p_dtype, rows_per_group, unit_offset, eps, y, ldy,
+                        y_dtype, mean=0, rstd=0, stream=0):
+    return lib.nomas_layernorm_fwd(x, rows, cols, ldx, x_dtype, w or None, b or None, ldp, p_dtype, rows_per_group,
+                                   int(unit_offset), eps, y, ldy, y_dtype, mean or None, rstd or None, stream or None)
+
+
+def nomas_layernorm_workspace_bytes(rows, cols, rows_per_group):
+    return lib.nomas_layernorm_workspace_bytes(rows, cols, rows_per_group)
+
+
+def nomas_layernorm_bwd(dy, lddy, y_dtype, x, ldx, x_dtype, rows, cols, w, ldp, p_dtype, rows_per_group, unit_offset,
+                        mean, rstd, dx, lddx, dw, db, ldg, workspace, stream=0):
+    return lib.nomas_layernorm_bwd(dy, lddy, y_dtype, x, ldx, x_dtype, rows, cols, w or None, ldp, p_dtype,
+                                   rows_per_group, int(unit_offset), mean, rstd, dx or None, lddx, dw or None,
+                                   db or None, ldg, workspace or None, stream or None)
+
+
+def nomas_w4_quantize(w, n_out, k_in, ldw, group, codes, scales, stream=0):
+    return lib.nomas_w4_quantize(w, n_out, k_in, ldw, group, codes, scales, stream or None)
+
+
+def nomas_w4_dequant(codes, scales, group, n_out, k_in, w, stream=0):
+    return lib.nomas_w4_dequant(codes, scales, group, n_out, k_in, w, stream or None)
+
+
+def nomas_w4a16_workspace_bytes(m, n_out, k_in):
+    return lib.nomas_w4a16_workspace_bytes(m, n_out, k_in)
+
+
+def nomas_w4a16_linear(x, m, k_in, ldx, codes, scales, group, n_out, y, ldy, y_dtype, workspace, status, stream=0):
+    return lib.nomas_w4a16_linear(x, m, k_in, ldx, codes, scales, group, n_out, y, ldy, y_dtype, workspace or None,
+                                  status, stream or None)

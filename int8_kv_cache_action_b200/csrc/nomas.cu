@@ -41,6 +41,31 @@ int bind_device(const nomas_kv_cache *c) {
     return e == cudaSuccess ? NOMAS_OK : cuda_fail("cudaSetDevice", (int)e, cudaGetErrorString(e));
 }
 
+DeviceScope::DeviceScope(const void *p) : rc(NOMAS_OK), previous(-1) {
+    cudaPointerAttributes at;
+    cudaError_t e = cudaPointerGetAttributes(&at, p);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        rc = cuda_fail("cudaPointerGetAttributes", (int)e, cudaGetErrorString(e));
+        return;
+    }
+    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) {
+        rc = NOMAS_EINVAL;
+        return;
+    }
+    int cur = -1;
+    if (cudaGetDevice(&cur) == cudaSuccess && cur == at.device) return;
+    e = cudaSetDevice(at.device);
+    if (e != cudaSuccess)
+        rc = cuda_fail("cudaSetDevice", (int)e, cudaGetErrorString(e));
+    else
+        previous = cur;
+}
+
+DeviceScope::~DeviceScope() {
+    if (previous >= 0) cudaSetDevice(previous);
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

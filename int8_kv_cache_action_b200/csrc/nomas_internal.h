@@ -166,6 +166,17 @@ int check_launch(const char *what);
 // Make the cache's device current for this thread (the library links its own CUDA runtime).
 int bind_device(const nomas_kv_cache *c);
 
+// For calls without a cache handle: makes the device that holds `p` current until the end of the scope.
+// rc is NOMAS_EINVAL for host memory, NOMAS_ECUDA for a failing CUDA call.
+struct DeviceScope {
+    explicit DeviceScope(const void *p);
+    ~DeviceScope();
+    DeviceScope(const DeviceScope &) = delete;
+    DeviceScope &operator=(const DeviceScope &) = delete;
+    int rc;
+    int previous;   // device to make current again, -1: none
+};
+
 // Limit of every bounded device wait (nomas_set_wait_limit_ns), in nanoseconds.
 uint64_t wait_limit_ns();
 

@@ -1,0 +1,561 @@
+// Layer norm with a weight and bias row per group of rows, forward and backward (definition in nomas.h):
+// the norm and modulation in front of the DiT's linear layers.
+//
+// Both directions are bound by HBM: the forward pass reads x and writes y, the backward pass reads dy and
+// x and writes dx, about 8 and 14 flops a value.  A row stays in the registers of a team of threads (a
+// power of two), so that the variance is a second sum over registers (exact differences, no sum of squares
+// that cancels) and memory is read once.
+//   layernorm_fwd_kernel   one row per team
+//   layernorm_bwd_kernel   a CTA takes a contiguous share of the rows, R rows of each team at a time; a
+//                          thread owns columns, so dw and db of a group add up in its registers in row
+//                          order.  Groups inside a share are written at once; where a group goes on in
+//                          the next share, its sums so far go to the workspace (two slots a CTA).
+//   layernorm_grad_kernel  adds up the shares of such groups, in share order.
+#include "common.cuh"
+
+namespace nomas {
+
+constexpr int kNormThreads = 256;
+
+struct NormParams {
+    const void *x, *w, *b;
+    void *y;
+    float *mean, *rstd;
+    int64_t ldx, ldy, ldp;
+    uint32_t rows, cols;
+    FastDiv group;              // rows of a group
+    int32_t team_log2;          // log2(threads of a team)
+    int32_t p_bf16;
+    float unit, eps;
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+// CH consecutive values at p + i as fp32, one wide access for CH = 4 or 8.
+template <int CH>
+__device__ __forceinline__ void load_chunk(const __nv_bfloat16 *p, float (&v)[CH]) {
+    if constexpr (CH == 1) {
+        v[0] = __bfloat162float(*p);
+    } else if constexpr (CH == 4) {
+        const uint2 c = *reinterpret_cast<const uint2 *>(p);
+        v[0] = bf16_lo(c.x), v[1] = bf16_hi(c.x), v[2] = bf16_lo(c.y), v[3] = bf16_hi(c.y);
+    } else {
+        const uint4 c = *reinterpret_cast<const uint4 *>(p);
+        v[0] = bf16_lo(c.x), v[1] = bf16_hi(c.x), v[2] = bf16_lo(c.y), v[3] = bf16_hi(c.y);
+        v[4] = bf16_lo(c.z), v[5] = bf16_hi(c.z), v[6] = bf16_lo(c.w), v[7] = bf16_hi(c.w);
+    }
+}
+template <int CH>
+__device__ __forceinline__ void load_chunk(const float *p, float (&v)[CH]) {
+    if constexpr (CH == 1) {
+        v[0] = *p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH; i += 4) {
+            const float4 c = *reinterpret_cast<const float4 *>(p + i);
+            v[i] = c.x, v[i + 1] = c.y, v[i + 2] = c.z, v[i + 3] = c.w;
+        }
+    }
+}
+template <int CH>
+__device__ __forceinline__ void store_chunk(__nv_bfloat16 *p, const float (&v)[CH]) {
+    if constexpr (CH == 1)
+        *p = __float2bfloat16_rn(v[0]);
+    else if constexpr (CH == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]));
+    else
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]), bf16x2_of(v[4], v[5]), bf16x2_of(v[6], v[7]));
+}
+template <int CH>
+__device__ __forceinline__ void store_chunk(float *p, const float (&v)[CH]) {
+    if constexpr (CH == 1) {
+        *p = v[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH; i += 4)
+            *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+}
+
+// A row of w or b (bf16 or fp32).
+template <int CH>
+__device__ __forceinline__ void load_param(const void *base, int32_t bf16, int64_t at, float (&v)[CH]) {
+    if (bf16)
+        load_chunk<CH>(static_cast<const __nv_bfloat16 *>(base) + at, v);
+    else
+        load_chunk<CH>(static_cast<const float *>(base) + at, v);
+}
+
+// Sum of N values over a team of 2^log2 threads; every thread gets it, in an order that depends on the
+// team alone.  Teams of more than a warp meet in `red` (N floats per warp and parity); all threads of the
+// CTA call it equally often.
+template <int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], int log2, float *red, int &parity) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        if (off >> log2) break;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+    }
+    if (log2 <= 5) return;
+    const int warp = threadIdx.x >> 5, warps = 1 << (log2 - 5), first = warp & ~(warps - 1);
+    float *r = red + parity * (int)(blockDim.x >> 5) * N;
+    parity ^= 1;                // the next sum's writes do not meet this one's reads
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[warp * N + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    for (int k = 0; k < warps; ++k) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += r[(first + k) * N + i];
+    }
+}
+
+template <typename TX, typename TY, int CH, int NV>
+__global__ void __launch_bounds__(kNormThreads) layernorm_fwd_kernel(const NormParams p) {
+    __shared__ float red[2 * kNormThreads / 32];
+    const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1);
+    const int64_t row = ((int64_t)blockIdx.x * kNormThreads + threadIdx.x) >> p.team_log2;
+    const bool live = row < p.rows;
+    const TX *x = static_cast<const TX *>(p.x) + row * p.ldx;
+    float v[NV][CH];
+    int parity = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const uint32_t c = (uint32_t)(lane + j * team) * CH;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) v[j][i] = 0.0f;
+        if (live && c < p.cols) load_chunk<CH>(x + c, v[j]);
+    }
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < CH; ++i) s[0] += v[j][i];
+    team_sum<1>(s, p.team_log2, red, parity);
+    const float mean = s[0] / (float)p.cols;
+    s[0] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const bool in = (uint32_t)(lane + j * team) * CH < p.cols;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            v[j][i] -= mean;
+            if (in) s[0] = fmaf(v[j][i], v[j][i], s[0]);
+        }
+    }
+    team_sum<1>(s, p.team_log2, red, parity);
+    const float rstd = 1.0f / sqrtf(s[0] / (float)p.cols + p.eps);
+    if (!live) return;
+    if (lane == 0) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    const int64_t pg = (int64_t)fdiv((uint32_t)row, p.group) * p.ldp;
+    TY *y = static_cast<TY *>(p.y) + row * p.ldy;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const uint32_t c = (uint32_t)(lane + j * team) * CH;
+        if (c >= p.cols) continue;
+        float w[CH], b[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) w[i] = 1.0f - p.unit, b[i] = 0.0f;
+        if (p.w) load_param<CH>(p.w, p.p_bf16, pg + c, w);
+        if (p.b) load_param<CH>(p.b, p.p_bf16, pg + c, b);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) w[i] = fmaf(v[j][i] * rstd, p.unit + w[i], b[i]);
+        store_chunk<CH>(y + c, w);
+    }
+}
+
+struct NormBwdParams {
+    const void *dy, *x, *w;
+    const float *mean, *rstd;
+    void *dx;
+    float *dw, *db, *part;      // part: [CTAs][2][2][cols] (share, head or tail of it, dw or db)
+    int64_t lddy, ldx, lddx, ldp, ldg;
+    uint32_t rows, cols, share; // share: rows of a CTA
+    FastDiv group;
+    int32_t team_log2, p_bf16;
+    float unit;
+};
+
+// dw and db of a group (or of a part of one) from the CTA's threads: teams of the CTA hold the same columns.
+template <int CH, int NV, int T>
+__device__ __forceinline__ void flush_grads(const NormBwdParams &p, float (&aw)[NV][CH], float (&ab)[NV][CH], float *dw,
+                                            float *db, float *meet) {
+    const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), teams = T >> p.team_log2;
+    if (NV == 1 && teams > 1) { // a larger NV has one team
+        const int stride = team * CH * NV, mine = threadIdx.x >> p.team_log2;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+                    meet[mine * stride + (j * CH + i) * team + lane] = g ? ab[j][i] : aw[j][i];
+            __syncthreads();
+            if (mine == 0) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        float s = 0.0f;
+                        for (int k = 0; k < teams; ++k) s += meet[k * stride + (j * CH + i) * team + lane];
+                        (g ? ab[j][i] : aw[j][i]) = s;
+                    }
+            }
+        }
+    }
+    if (threadIdx.x < team) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t c = (uint32_t)(lane + j * team) * CH;
+            if (c >= p.cols) continue;
+            // gradient rows of any pitch: element stores
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                if (dw) dw[c + i] = aw[j][i];
+                if (db) db[c + i] = ab[j][i];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < CH; ++i) aw[j][i] = ab[j][i] = 0.0f;
+}
+
+template <typename TX, typename TY, int CH, int NV, int R, int T>
+__global__ void __launch_bounds__(T) layernorm_bwd_kernel(const NormBwdParams p) {
+    __shared__ float red[2 * (T / 32) * 2 * R];
+    __shared__ float meet[NV == 1 ? T * CH : 1];
+    const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), mine = threadIdx.x >> p.team_log2;
+    const uint32_t teams = T >> p.team_log2;
+    const uint32_t begin = blockIdx.x * p.share, end = min(p.rows, begin + p.share);
+    float aw[NV][CH], ab[NV][CH];
+    int parity = 0;
+    const float inv = 1.0f / (float)p.cols;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < CH; ++i) aw[j][i] = ab[j][i] = 0.0f;
+    for (uint32_t row = begin; row < end;) {
+        const uint32_t g = fdiv(row, p.group);
+        const int64_t g0 = (int64_t)g * p.group.d, g1 = min(g0 + (int64_t)p.group.d, (int64_t)p.rows);
+        const uint32_t stop = (uint32_t)min((int64_t)end, g1);
+        const int64_t pg = (int64_t)g * p.ldp;
+        for (uint32_t r0 = row; r0 < stop; r0 += teams * R) {
+            float xh[R][NV][CH], gy[R][NV][CH], s[2 * R], rstd[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t at = r0 + r * teams + mine;
+                const bool live = at < stop;
+                const TX *x = static_cast<const TX *>(p.x) + (int64_t)at * p.ldx;
+                const TY *dy = static_cast<const TY *>(p.dy) + (int64_t)at * p.lddy;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const uint32_t c = (uint32_t)(lane + j * team) * CH;
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) xh[r][j][i] = gy[r][j][i] = 0.0f;
+                    if (live && c < p.cols) {
+                        load_chunk<CH>(x + c, xh[r][j]);
+                        load_chunk<CH>(dy + c, gy[r][j]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t at = r0 + r * teams + mine;
+                const bool live = at < stop;
+                const float mean = live ? __ldg(p.mean + at) : 0.0f;
+                rstd[r] = live ? __ldg(p.rstd + at) : 0.0f;
+                s[2 * r] = s[2 * r + 1] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const uint32_t c = (uint32_t)(lane + j * team) * CH;
+                    if (!live || c >= p.cols) continue;
+                    float w[CH];
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) w[i] = 1.0f - p.unit;
+                    if (p.w) load_param<CH>(p.w, p.p_bf16, pg + c, w);
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        const float xv = (xh[r][j][i] - mean) * rstd[r], d = gy[r][j][i];
+                        aw[j][i] = fmaf(d, xv, aw[j][i]);
+                        ab[j][i] += d;
+                        const float gv = d * (p.unit + w[i]);
+                        s[2 * r] += gv;
+                        s[2 * r + 1] = fmaf(gv, xv, s[2 * r + 1]);
+                        xh[r][j][i] = xv;
+                        gy[r][j][i] = gv;
+                    }
+                }
+            }
+            if (!p.dx) continue;
+            team_sum<2 * R>(s, p.team_log2, red, parity);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t at = r0 + r * teams + mine;
+                if (at >= stop) continue;
+                TX *dx = static_cast<TX *>(p.dx) + (int64_t)at * p.lddx;
+                const float m1 = s[2 * r] * inv, m2 = s[2 * r + 1] * inv;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const uint32_t c = (uint32_t)(lane + j * team) * CH;
+                    if (c >= p.cols) continue;
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) gy[r][j][i] = rstd[r] * (gy[r][j][i] - m1 - xh[r][j][i] * m2);
+                    store_chunk<CH>(dx + c, gy[r][j]);
+                }
+            }
+        }
+        if (p.dw || p.db) {
+            float *dw, *db;
+            if (g0 >= begin && g1 <= end) {
+                dw = p.dw ? p.dw + (int64_t)g * p.ldg : nullptr;
+                db = p.db ? p.db + (int64_t)g * p.ldg : nullptr;
+            } else {            // slot 0: the group began in an earlier share, 1: it goes on in a later one
+                dw = p.part + ((int64_t)blockIdx.x * 2 + (g0 < begin ? 0 : 1)) * 2 * p.cols;
+                db = dw + p.cols;
+            }
+            flush_grads<CH, NV, T>(p, aw, ab, dw, db, meet);
+        }
+        row = stop;
+    }
+}
+
+// Groups that several shares hold: the CTAs of row y of the grid add up the group that begins in share y
+// and goes on behind it, if there is one.  32 columns of dw or of db a CTA, kGradRows shares at a time.
+constexpr int kGradRows = 16;
+
+__global__ void __launch_bounds__(32 * kGradRows) layernorm_grad_kernel(const NormBwdParams p) {
+    __shared__ float red[kGradRows][33];
+    griddep_wait();
+    const int64_t begin = (int64_t)blockIdx.y * p.share, end = min((int64_t)p.rows, begin + p.share);
+    const uint32_t g = fdiv((uint32_t)(end - 1), p.group);
+    const int64_t g0 = (int64_t)g * p.group.d, g1 = min(g0 + (int64_t)p.group.d, (int64_t)p.rows);
+    if (g0 < begin || g1 <= end) return;
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t at = (int64_t)blockIdx.x * 32 + lane;         // 0 .. 2 cols - 1: dw then db
+    const int64_t last = (g1 - 1) / p.share;
+    float s = 0.0f;
+    if (at < 2 * (int64_t)p.cols)
+        for (int64_t b = blockIdx.y + k; b <= last; b += kGradRows)
+            s += p.part[(b * 2 + (b == blockIdx.y ? 1 : 0)) * 2 * p.cols + at];
+    red[k][lane] = s;
+    __syncthreads();
+    if (k != 0 || at >= 2 * (int64_t)p.cols) return;
+#pragma unroll
+    for (int i = 1; i < kGradRows; ++i) s += red[i][lane];
+    float *out = at < p.cols ? p.dw : p.db;
+    if (out) out[(int64_t)g * p.ldg + (at < p.cols ? at : at - p.cols)] = s;
+}
+
+// ------------------------------------------------------------------------------------------------
+// host
+// ------------------------------------------------------------------------------------------------
+
+static bool dtype_ok(int t) { return t == NOMAS_DTYPE_F32 || t == NOMAS_DTYPE_BF16; }
+static int dtype_size(int t) { return t == NOMAS_DTYPE_BF16 ? 2 : 4; }
+
+// A matrix operand: element aligned, pitch at least the row.
+static bool matrix_ok(const void *p, int64_t cols, int64_t ld, int dtype) {
+    return p && reinterpret_cast<uintptr_t>(p) % dtype_size(dtype) == 0 && ld >= cols;
+}
+static bool wide_ok(const void *p, int64_t ld) { return !p || (aligned16(p) && ld % 8 == 0); }
+
+static int check_norm(int64_t rows, int64_t cols, int64_t rows_per_group) {
+    if (rows < 0 || cols < 1 || rows_per_group < 0) return NOMAS_EINVAL;
+    if (cols > NOMAS_NORM_MAX_COLS || rows >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
+    return NOMAS_OK;
+}
+
+// Rows of a group as a divisor below 2^31 (one group: any divisor above the last row).
+static FastDiv group_div(int64_t rows, int64_t rows_per_group) {
+    const int64_t most = ((int64_t)1 << 31) - 1;
+    const int64_t d = rows_per_group == 0 ? rows : rows_per_group;
+    return make_fastdiv((uint32_t)(d < 1 ? 1 : d > most ? most : d));
+}
+
+static int log2_at_least(int64_t v) {
+    int l = 0;
+    while (((int64_t)1 << l) < v) ++l;
+    return l;
+}
+
+// Threads of a team (log2) for `chunks` chunks of a row, at most `per` of them a thread and 2^most threads:
+// whole warps as soon as a row fills one.
+static int team_of(int64_t chunks, int per, int most) {
+    int l = log2_at_least((chunks + per - 1) / per);
+    const int full = log2_at_least(chunks);
+    if (l < 5) l = full < 5 ? full : 5;
+    return l > most ? most : l;
+}
+
+template <typename TX, typename TY, int CH, int NV>
+static int launch_fwd(const NormParams &p, cudaStream_t st) {
+    const int64_t threads = (int64_t)p.rows << p.team_log2;
+    layernorm_fwd_kernel<TX, TY, CH, NV>
+        <<<(unsigned)((threads + kNormThreads - 1) / kNormThreads), kNormThreads, 0, st>>>(p);
+    return check_launch("layernorm_fwd_kernel launch");
+}
+
+// Chunks of a thread: up to 64 values (one row in a team's registers).  Few rows take the largest team
+// instead (256 threads): the row's loads are then in flight at once and the call is latency.
+template <typename TX, typename TY, int CH>
+static int pick_fwd(NormParams &p, cudaStream_t st) {
+    const int64_t chunks = (p.cols + CH - 1) / CH;
+    const bool few = p.rows <= (uint32_t)(2 * sm_count());
+    p.team_log2 = team_of(chunks, few ? 1 : 64 / CH, 8);
+    const int64_t nv = (chunks + (1 << p.team_log2) - 1) >> p.team_log2;
+    if (nv <= 1) return launch_fwd<TX, TY, CH, 1>(p, st);
+    if (nv <= 2) return launch_fwd<TX, TY, CH, 2>(p, st);
+    if (nv <= 4) return launch_fwd<TX, TY, CH, 4>(p, st);
+    if (CH == 8 || nv <= 8) return launch_fwd<TX, TY, CH, 8>(p, st);
+    if (CH == 4 || nv <= 16) return launch_fwd<TX, TY, CH, CH == 8 ? 8 : 16>(p, st);
+    return launch_fwd<TX, TY, CH, CH == 1 ? 64 : 8>(p, st);
+}
+
+template <typename TX, typename TY>
+static int wide_or_narrow_fwd(NormParams &p, bool wide, cudaStream_t st) {
+    constexpr int CH = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;     // 16 bytes of the wider type
+    return wide ? pick_fwd<TX, TY, CH>(p, st) : pick_fwd<TX, TY, 1>(p, st);
+}
+
+// Shares of the backward pass: the CTAs that the device holds at once, each with at least a round of rows.
+static void bwd_shares(int64_t rows, int64_t cols, int64_t *share, int64_t *ctas) {
+    const int64_t most = 2 * (int64_t)sm_count(), least = cols <= 512 ? 16 : 4;
+    int64_t s = (rows + most - 1) / most;
+    if (s < least) s = least;
+    *share = s;
+    *ctas = (rows + s - 1) / s;
+}
+
+template <typename TX, typename TY, int CH, int NV, int R, int T>
+static int launch_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
+    layernorm_bwd_kernel<TX, TY, CH, NV, R, T><<<(unsigned)ctas, T, 0, st>>>(p);
+    int rc = check_launch("layernorm_bwd_kernel launch");
+    if (rc || ctas == 1 || (!p.dw && !p.db)) return rc;
+    const dim3 grid((unsigned)((2 * (int64_t)p.cols + 31) / 32), (unsigned)(ctas - 1));
+    const cudaError_t e = launch_pdl(layernorm_grad_kernel, grid, dim3(32 * kGradRows), 0, st, p);
+    return e == cudaSuccess ? NOMAS_OK : cuda_fail("layernorm_grad_kernel launch", (int)e, cudaGetErrorString(e));
+}
+
+template <typename TX, typename TY, int CH>
+static int pick_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
+    const int64_t chunks = (p.cols + CH - 1) / CH;
+    p.team_log2 = team_of(chunks, 1, 8);
+    const int64_t values = ((chunks + 255) >> 8) * CH;
+    if (chunks <= 256) return launch_bwd<TX, TY, CH, 1, 4, 256>(p, ctas, st);
+    if (values <= 8) return launch_bwd<TX, TY, CH, 8 / CH, 4, 256>(p, ctas, st);
+    if (values <= 16) return launch_bwd<TX, TY, CH, 16 / CH, 2, 256>(p, ctas, st);
+    p.team_log2 = 9;
+    if (values <= 32) return launch_bwd<TX, TY, CH, 16 / CH, 1, 512>(p, ctas, st);
+    return launch_bwd<TX, TY, CH, 32 / CH, 1, 512>(p, ctas, st);
+}
+
+template <typename TX, typename TY>
+static int wide_or_narrow_bwd(NormBwdParams &p, bool wide, int64_t ctas, cudaStream_t st) {
+    constexpr int CH = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
+    return wide ? pick_bwd<TX, TY, CH>(p, ctas, st) : pick_bwd<TX, TY, 1>(p, ctas, st);
+}
+
+}  // namespace nomas
+
+using namespace nomas;
+
+extern "C" int nomas_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int64_t ldx, int x_dtype, const void *w,
+                                   const void *b, int64_t ldp, int p_dtype, int64_t rows_per_group, int unit_offset,
+                                   float eps, void *y, int64_t ldy, int y_dtype, float *mean, float *rstd,
+                                   nomas_stream stream) {
+    if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype) || !dtype_ok(p_dtype)) return NOMAS_EINVAL;
+    int rc = check_norm(rows, cols, rows_per_group);
+    if (rc) return rc;
+    if (!matrix_ok(x, cols, ldx, x_dtype) || !matrix_ok(y, cols, ldy, y_dtype) || !(eps >= 0.0f)) return NOMAS_EINVAL;
+    if ((w && !matrix_ok(w, cols, ldp, p_dtype)) || (b && !matrix_ok(b, cols, ldp, p_dtype))) return NOMAS_EINVAL;
+    if (reinterpret_cast<uintptr_t>(mean) % 4 != 0 || reinterpret_cast<uintptr_t>(rstd) % 4 != 0) return NOMAS_EINVAL;
+    if (x == y && (ldx != ldy || x_dtype != y_dtype)) return NOMAS_EINVAL;
+    if (rows == 0) return NOMAS_OK;
+    NormParams p{};
+    p.x = x, p.w = w, p.b = b, p.y = y, p.mean = mean, p.rstd = rstd;
+    p.ldx = ldx, p.ldy = ldy, p.ldp = ldp;
+    p.rows = (uint32_t)rows, p.cols = (uint32_t)cols;
+    p.group = group_div(rows, rows_per_group);
+    p.p_bf16 = p_dtype == NOMAS_DTYPE_BF16;
+    p.unit = unit_offset && w ? 1.0f : 0.0f;
+    p.eps = eps;
+    const bool wide = cols % 8 == 0 && wide_ok(x, ldx) && wide_ok(y, ldy) && wide_ok(w, ldp) && wide_ok(b, ldp);
+    DeviceScope dev(x);
+    if (dev.rc) return dev.rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (x_dtype == NOMAS_DTYPE_BF16)
+        return y_dtype == NOMAS_DTYPE_BF16 ? wide_or_narrow_fwd<__nv_bfloat16, __nv_bfloat16>(p, wide, st)
+                                           : wide_or_narrow_fwd<__nv_bfloat16, float>(p, wide, st);
+    return y_dtype == NOMAS_DTYPE_BF16 ? wide_or_narrow_fwd<float, __nv_bfloat16>(p, wide, st)
+                                       : wide_or_narrow_fwd<float, float>(p, wide, st);
+}
+
+extern "C" size_t nomas_layernorm_workspace_bytes(int64_t rows, int64_t cols, int64_t rows_per_group) {
+    if (check_norm(rows, cols, rows_per_group)) return 0;
+    int64_t share, ctas;
+    bwd_shares(rows, cols, &share, &ctas);
+    const size_t n = ctas > 1 ? (size_t)ctas * 4 * (size_t)cols * sizeof(float) : 0;
+    return n < 16 ? 16 : n;
+}
+
+extern "C" int nomas_layernorm_bwd(const void *dy, int64_t lddy, int y_dtype, const void *x, int64_t ldx, int x_dtype,
+                                   int64_t rows, int64_t cols, const void *w, int64_t ldp, int p_dtype,
+                                   int64_t rows_per_group, int unit_offset, const float *mean, const float *rstd,
+                                   void *dx, int64_t lddx, float *dw, float *db, int64_t ldg, void *workspace,
+                                   nomas_stream stream) {
+    if (!dtype_ok(x_dtype) || !dtype_ok(y_dtype) || !dtype_ok(p_dtype)) return NOMAS_EINVAL;
+    int rc = check_norm(rows, cols, rows_per_group);
+    if (rc) return rc;
+    if (!matrix_ok(dy, cols, lddy, y_dtype) || !matrix_ok(x, cols, ldx, x_dtype) || !mean || !rstd) return NOMAS_EINVAL;
+    if (reinterpret_cast<uintptr_t>(mean) % 4 != 0 || reinterpret_cast<uintptr_t>(rstd) % 4 != 0) return NOMAS_EINVAL;
+    if (!dx && !dw && !db) return NOMAS_EINVAL;
+    if ((w && !matrix_ok(w, cols, ldp, p_dtype)) || (dx && !matrix_ok(dx, cols, lddx, x_dtype))) return NOMAS_EINVAL;
+    if ((dw && !matrix_ok(dw, cols, ldg, NOMAS_DTYPE_F32)) || (db && !matrix_ok(db, cols, ldg, NOMAS_DTYPE_F32)))
+        return NOMAS_EINVAL;
+    if (dx && ((dx == x && lddx != ldx) || (dx == dy && (lddx != lddy || x_dtype != y_dtype)))) return NOMAS_EINVAL;
+    if ((dw || db) && (!workspace || !aligned16(workspace))) return NOMAS_EINVAL;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    DeviceScope dev(x);
+    if (dev.rc) return dev.rc;
+    if (rows == 0) {
+        for (float *out : {dw, db}) {
+            if (!out || rows_per_group != 0) continue;
+            const cudaError_t e = cudaMemsetAsync(out, 0, (size_t)cols * sizeof(float), st);
+            if (e != cudaSuccess) return cuda_fail("cudaMemsetAsync", (int)e, cudaGetErrorString(e));
+        }
+        return NOMAS_OK;
+    }
+    NormBwdParams p{};
+    int64_t share, ctas;
+    bwd_shares(rows, cols, &share, &ctas);
+    p.dy = dy, p.x = x, p.w = w, p.mean = mean, p.rstd = rstd, p.dx = dx, p.dw = dw, p.db = db;
+    p.part = static_cast<float *>(workspace);
+    p.lddy = lddy, p.ldx = ldx, p.lddx = lddx, p.ldp = ldp, p.ldg = ldg;
+    p.rows = (uint32_t)rows, p.cols = (uint32_t)cols, p.share = (uint32_t)share;
+    p.group = group_div(rows, rows_per_group);
+    p.p_bf16 = p_dtype == NOMAS_DTYPE_BF16;
+    p.unit = unit_offset && w ? 1.0f : 0.0f;
+    const bool wide = cols % 8 == 0 && wide_ok(dy, lddy) && wide_ok(x, ldx) && wide_ok(w, ldp) && wide_ok(dx, lddx);
+    if (x_dtype == NOMAS_DTYPE_BF16)
+        return y_dtype == NOMAS_DTYPE_BF16 ? wide_or_narrow_bwd<__nv_bfloat16, __nv_bfloat16>(p, wide, ctas, st)
+                                           : wide_or_narrow_bwd<__nv_bfloat16, float>(p, wide, ctas, st);
+    return y_dtype == NOMAS_DTYPE_BF16 ? wide_or_narrow_bwd<float, __nv_bfloat16>(p, wide, ctas, st)
+                                       : wide_or_narrow_bwd<float, float>(p, wide, ctas, st);
+}

@@ -1,0 +1,364 @@
+// Rotary positions with several axes (definition in nomas.h): the elementwise step between the QKV
+// projection and the append / attention.
+//
+// A call reads and writes every value once and is bound by HBM: 3 flops a value against 2 x 2 bytes.
+// What a token's heads share is its D / 2 sines and cosines, so a CTA takes all heads of a few tokens,
+// issues its loads first, computes the tokens' table while they are in flight (one fp64 product and
+// reduction and one fp32 sincospi per pair: 64 for 2 x 16 x 128 values of q and k) and reads it from
+// shared memory.  No table in global memory, so nothing to keep between calls.
+#include <cmath>
+
+#include "common.cuh"
+
+namespace nomas {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 4;                 // 16-byte chunks (chunk pairs) in flight per thread
+constexpr int kRopeTable = 2048;               // (cos, sin) entries of a CTA's tokens: 16 KB
+constexpr int kRopeMaxPairs = NOMAS_ROPE_MAX_HEAD_DIM / 2;
+
+// How a 16-byte chunk finds the other value of its pairs: in itself (interleaved), in a second chunk that
+// the same thread holds (halves, where every axis' half is whole chunks), or anywhere in its row, through
+// shared memory (halves of other widths).
+enum RopeForm { kRopeInside = 0, kRopeTwoChunks = 1, kRopeGather = 2 };
+
+struct RopeTensor {
+    const char *x;
+    char *y;
+    int64_t x_tok, x_head, y_tok, y_head;      // bytes
+    uint32_t first_item;                       // items of a token in front of this tensor's
+};
+
+struct RopeParams {
+    double turns[kRopeMaxPairs];               // turns per unit of position, by pair
+    double origin[3], step[3];
+    RopeTensor t[NOMAS_ROPE_MAX_TENSORS];
+    const float *positions;                    // or null: the grid
+    FastDiv plane, width;                      // grid_h * grid_w, grid_w
+    FastDiv items;                             // items of a token, all tensors
+    FastDiv per_head;                          // items of a head
+    uint32_t tokens, tokens_per_cta, batch;    // batch: items that a CTA takes at a time
+    int32_t n_tensors, inverse;
+    int32_t axis_at[4];                        // first channel of each axis, end of the last
+    int32_t pairs, all_pairs;                  // pairs that turn, head_dim / 2
+};
+
+template <typename T>
+struct Chunk {
+    static constexpr int V = 16 / sizeof(T);
+};
+
+__device__ __forceinline__ void unpack(const uint4 &c, float (&v)[8]) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint4 &c, float (&v)[4]) {
+    v[0] = __uint_as_float(c.x), v[1] = __uint_as_float(c.y), v[2] = __uint_as_float(c.z), v[3] = __uint_as_float(c.w);
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+// The rotated chunk with the words behind its first `turned` channels as they were: channels that no axis
+// holds keep every bit (a conversion would change a NaN's).
+template <int V>
+__device__ __forceinline__ uint4 keep_behind(uint4 out, const uint4 &in, int turned) {
+    constexpr int per_word = V / 4;
+    if (turned <= 0 * per_word) out.x = in.x;
+    if (turned <= 1 * per_word) out.y = in.y;
+    if (turned <= 2 * per_word) out.z = in.z;
+    if (turned <= 3 * per_word) out.w = in.w;
+    return out;
+}
+
+// Where an item (one chunk, or the first of two) is read and written.
+struct RopeItem {
+    const char *x;
+    char *y;
+    uint32_t token, j;                         // token of the CTA, item of the head
+};
+
+__device__ __forceinline__ RopeItem rope_item(const RopeParams &p, uint32_t it, uint32_t token0) {
+    RopeItem r;
+    r.token = fdiv(it, p.items);
+    const uint32_t rest = it - r.token * p.items.d;
+    int k = 0;
+#pragma unroll
+    for (int i = 1; i < NOMAS_ROPE_MAX_TENSORS; ++i)
+        if (i < p.n_tensors && rest >= p.t[i].first_item) k = i;
+    const RopeTensor &t = p.t[k];
+    const uint32_t in = rest - t.first_item, head = fdiv(in, p.per_head);
+    r.j = in - head * p.per_head.d;
+    const int64_t tok = (int64_t)token0 + r.token;
+    r.x = t.x + tok * t.x_tok + (int64_t)head * t.x_head;
+    r.y = t.y + tok * t.y_tok + (int64_t)head * t.y_head;
+    return r;
+}
+
+// First channel of item j in the two-chunk form, and how far its second chunk is: item j holds pairs
+// j V .. j V + V - 1, whose axis starts at channel axis_at[a] = 2 x (pairs in front of it).  Behind the axes
+// the item is two neighbouring chunks that pass through.
+template <typename T>
+__device__ __forceinline__ void rope_two(const RopeParams &p, uint32_t j, uint32_t &c, uint32_t &apart) {
+    constexpr uint32_t V = Chunk<T>::V;
+    const uint32_t ch = 2 * V * j;
+    apart = V;
+    c = ch;
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+        const uint32_t s = p.axis_at[a], e = p.axis_at[a + 1];
+        if (ch >= s && ch < e) {
+            apart = (e - s) / 2;
+            c = s + (ch - s) / 2;
+        }
+    }
+}
+
+// The table of a CTA's tokens: (cos, sin) of each pair, sin negated for the inverse.
+__device__ __forceinline__ void rope_table(const RopeParams &p, uint32_t token0, uint32_t n, float2 *table) {
+    const uint32_t pairs = p.pairs;
+    for (uint32_t e = threadIdx.x; e < n * p.all_pairs; e += kRopeThreads) {
+        const uint32_t tok = e / (uint32_t)p.all_pairs, i = e - tok * p.all_pairs;
+        if (i >= pairs) continue;              // passes through: never read
+        const int a = 2 * (int)i < p.axis_at[1] ? 0 : 2 * (int)i < p.axis_at[2] ? 1 : 2;
+        double at;
+        if (p.positions) {
+            at = (double)__ldg(p.positions + 3 * (int64_t)(token0 + tok) + a);
+        } else {
+            const uint32_t f = fdiv(token0 + tok, p.plane), in = token0 + tok - f * p.plane.d;
+            const uint32_t row = fdiv(in, p.width), col = in - row * p.width.d;
+            at = fma(p.step[a], (double)(a == 0 ? f : a == 1 ? row : col), p.origin[a]);
+        }
+        // the angle in turns, its whole turns dropped in fp64: what is left keeps fp32's relative precision
+        const double turns = at * p.turns[i];
+        float s, c;
+        sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+        table[e] = make_float2(c, p.inverse ? -s : s);
+    }
+}
+
+__device__ __forceinline__ void turn(float &a, float &b, const float2 &cs) {
+    const float x = a, y = b;
+    a = fmaf(x, cs.x, -(y * cs.y));
+    b = fmaf(x, cs.y, y * cs.x);
+}
+
+template <typename T, int FORM>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int V = Chunk<T>::V, U = kRopeUnroll;
+    __shared__ __align__(16) float2 table[kRopeTable];
+    __shared__ __align__(16) uint4 rows[FORM == kRopeGather ? U * kRopeThreads : 1];
+    __shared__ int16_t pair_of[FORM == kRopeGather ? NOMAS_ROPE_MAX_HEAD_DIM : 1];      // -1: passes through
+    __shared__ int16_t other_of[FORM == kRopeGather ? NOMAS_ROPE_MAX_HEAD_DIM : 1];     // channel of the pair's other value
+
+    const uint32_t token0 = blockIdx.x * p.tokens_per_cta;
+    const uint32_t n = min(p.tokens_per_cta, p.tokens - token0);
+    const uint32_t items = n * p.items.d;
+    for (uint32_t base = 0; base < items; base += p.batch) {
+        const uint32_t end = min(items, base + p.batch);
+        RopeItem item[U];
+        uint4 v0[U], v1[FORM == kRopeTwoChunks ? U : 1];
+        uint32_t apart[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t it = base + u * kRopeThreads + threadIdx.x;
+            if (it >= end) continue;
+            item[u] = rope_item(p, it, token0);
+            if constexpr (FORM == kRopeTwoChunks) {
+                uint32_t c;
+                rope_two<T>(p, item[u].j, c, apart[u]);
+                item[u].x += c * sizeof(T);
+                item[u].y += c * sizeof(T);
+                v1[u] = *reinterpret_cast<const uint4 *>(item[u].x + apart[u] * sizeof(T));
+            } else {
+                item[u].x += item[u].j * 16;
+                item[u].y += item[u].j * 16;
+            }
+            v0[u] = *reinterpret_cast<const uint4 *>(item[u].x);
+        }
+        if (base == 0) {
+            rope_table(p, token0, n, table);
+            if constexpr (FORM == kRopeGather) {
+                for (int c = threadIdx.x; c < 2 * p.all_pairs; c += kRopeThreads) {
+                    int pair = -1, other = c;
+                    for (int a = 0; a < 3; ++a) {
+                        const int s = p.axis_at[a], e = p.axis_at[a + 1], half = (e - s) / 2;
+                        if (c < s || c >= e) continue;
+                        const bool second = c - s >= half;
+                        pair = s / 2 + (c - s) - (second ? half : 0);
+                        other = second ? c - half : c + half;
+                    }
+                    pair_of[c] = (int16_t)pair;
+                    other_of[c] = (int16_t)other;
+                }
+            }
+            __syncthreads();
+        }
+        if constexpr (FORM == kRopeGather) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) rows[u * kRopeThreads + threadIdx.x] = v0[u];
+            __syncthreads();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t it = base + u * kRopeThreads + threadIdx.x;
+            if (it >= end) continue;
+            const float2 *cs = table + item[u].token * p.all_pairs;
+            float a[V];
+            unpack(v0[u], a);
+            if constexpr (FORM == kRopeInside) {
+                const int i0 = item[u].j * (V / 2);
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i)
+                    if (i0 + i < p.pairs) turn(a[2 * i], a[2 * i + 1], cs[i0 + i]);
+                *reinterpret_cast<uint4 *>(item[u].y) = keep_behind<V>(pack(a), v0[u], 2 * (p.pairs - i0));
+            } else if constexpr (FORM == kRopeTwoChunks) {
+                const int i0 = item[u].j * V;
+                float b[V];
+                unpack(v1[u], b);
+                if (i0 < p.pairs) {            // whole items turn or pass
+#pragma unroll
+                    for (int i = 0; i < V; ++i) turn(a[i], b[i], cs[i0 + i]);
+                    v0[u] = pack(a);
+                    v1[u] = pack(b);
+                }
+                *reinterpret_cast<uint4 *>(item[u].y) = v0[u];
+                *reinterpret_cast<uint4 *>(item[u].y + apart[u] * sizeof(T)) = v1[u];
+            } else {
+                const T *row = reinterpret_cast<const T *>(rows + (it - base - item[u].j));
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int c = item[u].j * V + i, pair = pair_of[c], other = other_of[c];
+                    if (pair < 0) continue;
+                    const float2 t = cs[pair];
+                    const float o = (float)row[other];
+                    a[i] = other > c ? fmaf(a[i], t.x, -(o * t.y)) : fmaf(o, t.y, a[i] * t.x);
+                }
+                *reinterpret_cast<uint4 *>(item[u].y) = keep_behind<V>(pack(a), v0[u], 2 * p.pairs - (int)item[u].j * V);
+            }
+        }
+        if constexpr (FORM == kRopeGather) __syncthreads();
+    }
+}
+
+template <typename T>
+static int launch_rope(RopeForm form, unsigned grid, const RopeParams &p, cudaStream_t st) {
+    if (form == kRopeInside)
+        rope_kernel<T, kRopeInside><<<grid, kRopeThreads, 0, st>>>(p);
+    else if (form == kRopeTwoChunks)
+        rope_kernel<T, kRopeTwoChunks><<<grid, kRopeThreads, 0, st>>>(p);
+    else
+        rope_kernel<T, kRopeGather><<<grid, kRopeThreads, 0, st>>>(p);
+    return check_launch("rope_kernel launch");
+}
+
+static bool rope_spec_ok(const nomas_rope_spec *s) {
+    if (!s || s->head_dim < 8 || s->head_dim > NOMAS_ROPE_MAX_HEAD_DIM || s->head_dim % 8 != 0) return false;
+    if (s->pairing != NOMAS_ROPE_INTERLEAVED && s->pairing != NOMAS_ROPE_HALVES) return false;
+    if (!std::isfinite(s->theta) || s->theta <= 0.0) return false;
+    int64_t sum = 0;
+    for (int a = 0; a < 3; ++a) {
+        if (s->axis_dim[a] < 0 || s->axis_dim[a] % 2 != 0) return false;
+        sum += s->axis_dim[a];
+    }
+    return sum >= 2 && sum <= s->head_dim;
+}
+
+}  // namespace nomas
+
+using namespace nomas;
+
+extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *grid, const float *positions,
+                          int64_t tokens, const nomas_rope_tensor *tensors, int n_tensors, int dtype, int inverse,
+                          nomas_stream stream) {
+    if (!rope_spec_ok(spec) || !tensors || n_tensors < 1 || n_tensors > NOMAS_ROPE_MAX_TENSORS || tokens < 0)
+        return NOMAS_EINVAL;
+    if ((grid != nullptr) == (positions != nullptr)) return NOMAS_EINVAL;
+    if (dtype != NOMAS_DTYPE_F32 && dtype != NOMAS_DTYPE_BF16) return NOMAS_EINVAL;
+    RopeParams p{};
+    if (grid) {
+        if (grid->grid_h < 1 || grid->grid_w < 1 || (int64_t)grid->grid_h * grid->grid_w >= (int64_t)1 << 31)
+            return NOMAS_EINVAL;
+        for (int a = 0; a < 3; ++a) {
+            if (!std::isfinite(grid->origin[a]) || !std::isfinite(grid->step[a])) return NOMAS_EINVAL;
+            p.origin[a] = grid->origin[a];
+            p.step[a] = grid->step[a];
+        }
+        p.plane = make_fastdiv((uint32_t)(grid->grid_h * grid->grid_w));
+        p.width = make_fastdiv((uint32_t)grid->grid_w);
+    } else if (reinterpret_cast<uintptr_t>(positions) % 4 != 0) {
+        return NOMAS_EINVAL;
+    }
+    if (tokens >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
+
+    const int esize = dtype == NOMAS_DTYPE_BF16 ? 2 : 4, v = 16 / esize;
+    p.axis_at[0] = 0;
+    for (int a = 0; a < 3; ++a) p.axis_at[a + 1] = p.axis_at[a] + spec->axis_dim[a];
+    p.pairs = p.axis_at[3] / 2;
+    p.all_pairs = spec->head_dim / 2;
+    RopeForm form = kRopeInside;
+    if (spec->pairing == NOMAS_ROPE_HALVES) {
+        form = spec->head_dim % (2 * v) == 0 ? kRopeTwoChunks : kRopeGather;
+        for (int a = 0; a < 3; ++a)
+            if (spec->axis_dim[a] % (2 * v) != 0) form = kRopeGather;
+    }
+    const int64_t per_head = spec->head_dim / (form == kRopeTwoChunks ? 2 * v : v);
+    int64_t items = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+        const nomas_rope_tensor &t = tensors[i];
+        if (!t.x || !t.y || !aligned16(t.x) || !aligned16(t.y) || t.heads < 1) return NOMAS_EINVAL;
+        for (int64_t s : {t.x_tok_stride, t.x_head_stride, t.y_tok_stride, t.y_head_stride})
+            if (s % 8 != 0 || s < 0) return NOMAS_EINVAL;
+        // every value of y has a place of its own
+        if ((tokens > 1 && t.y_tok_stride < spec->head_dim) || (t.heads > 1 && t.y_head_stride < spec->head_dim))
+            return NOMAS_EINVAL;
+        if (t.x == t.y && (t.x_tok_stride != t.y_tok_stride || t.x_head_stride != t.y_head_stride)) return NOMAS_EINVAL;
+        p.t[i] = RopeTensor{static_cast<const char *>(t.x), static_cast<char *>(t.y), t.x_tok_stride * esize,
+                            t.x_head_stride * esize, t.y_tok_stride * esize, t.y_head_stride * esize, (uint32_t)items};
+        items += t.heads * per_head;
+        if (items >= (int64_t)1 << 24) return NOMAS_EUNSUPPORTED;
+    }
+    if (tokens == 0) return NOMAS_OK;
+    double at = 0.0;
+    int pair = 0;
+    for (int a = 0; a < 3; ++a)
+        for (int i = 0; i < spec->axis_dim[a] / 2; ++i, ++pair) {
+            at = std::pow(spec->theta, -2.0 * i / spec->axis_dim[a]);
+            p.turns[pair] = at / 6.283185307179586476925;
+        }
+    p.positions = positions;
+    p.items = make_fastdiv((uint32_t)items);
+    p.per_head = make_fastdiv((uint32_t)per_head);
+    p.tokens = (uint32_t)tokens;
+    p.n_tensors = n_tensors;
+    p.inverse = inverse != 0;
+    // a CTA takes as many tokens as fill one round of loads, as far as their table fits and every SM still
+    // gets a CTA
+    const int64_t round = (int64_t)kRopeUnroll * kRopeThreads;
+    int64_t per_cta = round / items;
+    const int64_t spread = (tokens + sm_count() - 1) / sm_count();
+    if (per_cta > kRopeTable / p.all_pairs) per_cta = kRopeTable / p.all_pairs;
+    if (per_cta > spread) per_cta = spread;
+    if (per_cta < 1) per_cta = 1;
+    p.tokens_per_cta = (uint32_t)per_cta;
+    // whole head rows a round: the gather form reads a row's other chunks
+    p.batch = (uint32_t)(round / per_head * per_head);
+    DeviceScope dev(tensors[0].x);
+    if (dev.rc) return dev.rc;
+    const unsigned ctas = (unsigned)((tokens + per_cta - 1) / per_cta);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == NOMAS_DTYPE_BF16 ? launch_rope<__nv_bfloat16>(form, ctas, p, st) : launch_rope<float>(form, ctas, p, st);
+}

@@ -1,0 +1,290 @@
+// Linear layer with 4-bit weights and group scales (definition in nomas.h).
+//
+// Kernels:
+//   w4_quantize_kernel  one warp per (row, group)
+//   w4_dequant_kernel   bf16(code * scale), 32 weights per thread (HBM-bound)
+//   w4_rows_kernel      y = x W^T for up to kW4MaxRows rows of x, every code read once: bound by the codes'
+//                       bytes, so the weights are widened in registers and go straight into the register
+//                       form of the tensor-core product (m16n8k16, 16 rows of W by 8 rows of x): one
+//                       instruction per 8 weights of a lane, where fp32 products would need one per
+//                       weight and row of x.  tcgen05 would want the widened weights in shared memory
+//                       first; it takes over (w4_dequant_kernel, nomas_linear_bf16) for more rows.
+#include "common.cuh"
+
+namespace nomas {
+
+constexpr int kW4MaxRows = 64;
+constexpr int kW4Warps = 8;                    // they share the columns of 16 rows of W
+
+// 8 codes (one word, code i in bits 4i .. 4i + 3) times a scale, as bf16 pairs (i, i + 4), i = 0 .. 3: with
+// u = code + 8 in the low bits of the mantissa of 128 (0x4300, whose last place is 1) the bf16 is 128 + u, the
+// code comes out of - 136 exactly, and the product with the scale is the one rounding.
+__device__ __forceinline__ void w4_widen(uint32_t word, __nv_bfloat162 scale, uint32_t (&out)[4]) {
+    const __nv_bfloat162 minus136 = __floats2bfloat162_rn(-136.0f, -136.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+        const __nv_bfloat162 w = __hmul2(__hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&u), minus136), scale);
+        out[i] = *reinterpret_cast<const uint32_t *>(&w);
+    }
+}
+
+// D += A B: A 16 x 16 (rows of W), B 16 x 8 (rows of x), bf16 operands, fp32 sums.
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct W4Params {
+    const uint8_t *codes;
+    const __nv_bfloat16 *scales;
+    const __nv_bfloat16 *x;
+    void *y;
+    int64_t ldx, ldy;
+    int64_t n;                                 // rows of W
+    int32_t m, k, groups, group_log2, y_bf16;
+};
+
+__device__ __forceinline__ uint4 load_stream(const void *p) {
+    uint4 v;
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// A CTA: rows n0 .. n0 + 15 of W, its warps chunks of 128 columns in turn.  In a chunk, lane 4 g + t holds
+// columns 32 t .. 32 t + 31 of rows g and g + 8 (16 bytes of codes each; the 32 columns have one scale) and of
+// row g of each 8 rows of x.  Which column of the chunk stands for which index of a product's inner dimension
+// is free as long as both operands agree: a product takes 4 consecutive-in-word pairs of every lane.
+template <int NT>
+__global__ void __launch_bounds__(32 * kW4Warps) w4_rows_kernel(const W4Params p) {
+    __shared__ float red[kW4Warps][NT * 8][17];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t r0 = min(n0 + g, p.n - 1), r1 = min(n0 + g + 8, p.n - 1);
+    const uint8_t *c0 = p.codes + r0 * (p.k / 2), *c1 = p.codes + r1 * (p.k / 2);
+    const __nv_bfloat16 *s0 = p.scales + r0 * p.groups, *s1 = p.scales + r1 * p.groups;
+    float acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    const int chunks = (p.k + 127) / 128;
+#pragma unroll 2
+    for (int c = warp; c < chunks; c += kW4Warps) {
+        const int col = c * 128 + 32 * t;
+        const bool in = col < p.k;             // K is a multiple of 32: a lane's columns are in or out
+        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+        __nv_bfloat16 f0 = __float2bfloat16_rn(0.0f), f1 = f0;
+        if (in) {
+            w0 = load_stream(c0 + col / 2);
+            w1 = load_stream(c1 + col / 2);
+            f0 = s0[col >> p.group_log2];
+            f1 = s1[col >> p.group_log2];
+        }
+        const __nv_bfloat162 sc0 = __halves2bfloat162(f0, f0), sc1 = __halves2bfloat162(f1, f1);
+        const uint32_t a[4] = {w0.x, w0.y, w0.z, w0.w}, b[4] = {w1.x, w1.y, w1.z, w1.w};
+        float part[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part[i][j] = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t u[4], v[4];
+            w4_widen(a[q], sc0, u);
+            w4_widen(b[q], sc1, v);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const int row = i * 8 + g;
+                uint4 xv = make_uint4(0, 0, 0, 0);
+                if (in && row < p.m) xv = __ldg(reinterpret_cast<const uint4 *>(p.x + (int64_t)row * p.ldx + col + 8 * q));
+                // pairs (0,4) (1,5) (2,6) (3,7) of 8 columns
+                const uint32_t x0 = __byte_perm(xv.x, xv.z, 0x5410), x1 = __byte_perm(xv.x, xv.z, 0x7632);
+                const uint32_t x2 = __byte_perm(xv.y, xv.w, 0x5410), x3 = __byte_perm(xv.y, xv.w, 0x7632);
+                mma_16x8x16(part[i], u[0], v[0], u[1], v[1], x0, x1);
+                mma_16x8x16(part[i], u[2], v[2], u[3], v[3], x2, x3);
+            }
+        }
+        // the tensor cores truncate sums; chunks of 128 columns are added up in rounded fp32
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] += part[i][j];
+    }
+    // acc: rows g and g + 8 of W, rows 8 i + 2 t and 8 i + 2 t + 1 of x
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        red[warp][i * 8 + 2 * t][g] = acc[i][0];
+        red[warp][i * 8 + 2 * t + 1][g] = acc[i][1];
+        red[warp][i * 8 + 2 * t][g + 8] = acc[i][2];
+        red[warp][i * 8 + 2 * t + 1][g + 8] = acc[i][3];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < NT * 8 * 16; e += 32 * kW4Warps) {
+        const int row = e >> 4, col = e & 15;
+        if (row >= p.m || n0 + col >= p.n) continue;
+        float s = red[0][row][col];
+#pragma unroll
+        for (int w = 1; w < kW4Warps; ++w) s += red[w][row][col];
+        if (p.y_bf16)
+            static_cast<__nv_bfloat16 *>(p.y)[(int64_t)row * p.ldy + n0 + col] = __float2bfloat16_rn(s);
+        else
+            static_cast<float *>(p.y)[(int64_t)row * p.ldy + n0 + col] = s;
+    }
+}
+
+__global__ void __launch_bounds__(256) w4_dequant_kernel(const uint8_t *codes, const __nv_bfloat16 *scales, int64_t total32,
+                                                         int32_t k32, int32_t groups, int32_t group_log2,
+                                                         __nv_bfloat16 *w) {
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total32; i += stride) {
+        const int64_t row = i / k32;
+        const int32_t col = (int32_t)(i - row * k32) * 32;
+        const __nv_bfloat16 f = scales[row * groups + (col >> group_log2)];
+        const __nv_bfloat162 s = __halves2bfloat162(f, f);
+        const uint4 c = load_stream(codes + i * 16);
+        const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+        uint4 *dst = reinterpret_cast<uint4 *>(w + i * 32);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t u[4];
+            w4_widen(word[q], s, u);
+            dst[q] = make_uint4(__byte_perm(u[0], u[1], 0x5410), __byte_perm(u[2], u[3], 0x5410),
+                                __byte_perm(u[0], u[1], 0x7632), __byte_perm(u[2], u[3], 0x7632));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16 *w, int64_t n, int32_t k, int64_t ldw,
+                                                          int32_t groups, int32_t group, uint8_t *codes,
+                                                          __nv_bfloat16 *scales) {
+    const int64_t at = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (at >= n * groups) return;
+    const int64_t row = at / groups;
+    const int32_t gr = (int32_t)(at - row * groups), k0 = gr * group, k1 = min(k, k0 + group);
+    const __nv_bfloat16 *src = w + row * ldw;
+    float a = 0.0f;
+    bool finite = true;
+    for (int32_t c = k0 + lane; c < k1; c += 32) {
+        const float v = fabsf(__bfloat162float(src[c]));
+        finite &= v <= 3.402823466e38f;
+        a = fmaxf(a, v);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+    finite = __all_sync(0xffffffffu, finite);
+    const __nv_bfloat16 sb = __float2bfloat16_rn(finite ? __fdiv_rn(a, 7.0f) : __int_as_float(0x7fffffff));
+    const float s = __bfloat162float(sb);
+    if (lane == 0) scales[at] = sb;
+    for (int32_t c = k0 + 2 * lane; c < k1; c += 64) {
+        uint32_t byte = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int code = 0;
+            if (s > 0.0f) code = (int)fminf(7.0f, fmaxf(-7.0f, rintf(__fdiv_rn(__bfloat162float(src[c + h]), s))));
+            byte |= (uint32_t)(code + 8) << (4 * h);
+        }
+        codes[row * (k / 2) + c / 2] = (uint8_t)byte;
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// host
+// ------------------------------------------------------------------------------------------------
+
+static int group_log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
+
+static int check_w4(const void *codes, const void *scales, int group, int64_t n_out, int64_t k_in) {
+    if (!codes || !scales || !aligned16(codes) || !aligned16(scales) || group_log2_of(group) < 0) return NOMAS_EINVAL;
+    if (n_out < 1 || k_in < 32 || k_in % 32 != 0) return NOMAS_EINVAL;
+    if (n_out >= (int64_t)1 << 31 || k_in >= (int64_t)1 << 30) return NOMAS_EUNSUPPORTED;
+    return NOMAS_OK;
+}
+
+static int enqueue_w4_dequant(const uint8_t *codes, const void *scales, int group, int64_t n_out, int64_t k_in, void *w,
+                              cudaStream_t st) {
+    const int64_t total = n_out * (k_in / 32), most = (int64_t)sm_count() * 8;
+    const int64_t blocks = (total + 255) / 256;
+    w4_dequant_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(
+        codes, static_cast<const __nv_bfloat16 *>(scales), total, (int32_t)(k_in / 32), (int32_t)((k_in + group - 1) / group),
+        group_log2_of(group), static_cast<__nv_bfloat16 *>(w));
+    return check_launch("w4_dequant_kernel launch");
+}
+
+template <int NT>
+static int launch_w4_rows(const W4Params &p, cudaStream_t st) {
+    w4_rows_kernel<NT><<<(unsigned)((p.n + 15) / 16), 32 * kW4Warps, 0, st>>>(p);
+    return check_launch("w4_rows_kernel launch");
+}
+
+}  // namespace nomas
+
+using namespace nomas;
+
+extern "C" int nomas_w4_quantize(const void *w, int64_t n_out, int64_t k_in, int64_t ldw, int group, uint8_t *codes,
+                                 void *scales, nomas_stream stream) {
+    int rc = check_w4(codes, scales, group, n_out, k_in);
+    if (rc) return rc;
+    if (!w || !aligned16(w) || ldw < k_in) return NOMAS_EINVAL;
+    const int64_t groups = (k_in + group - 1) / group;
+    if ((n_out * groups + 7) / 8 >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
+    DeviceScope dev(codes);
+    if (dev.rc) return dev.rc;
+    w4_quantize_kernel<<<(unsigned)((n_out * groups + 7) / 8), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        static_cast<const __nv_bfloat16 *>(w), n_out, (int32_t)k_in, ldw, (int32_t)groups, group, codes,
+        static_cast<__nv_bfloat16 *>(scales));
+    return check_launch("w4_quantize_kernel launch");
+}
+
+extern "C" int nomas_w4_dequant(const uint8_t *codes, const void *scales, int group, int64_t n_out, int64_t k_in, void *w,
+                                nomas_stream stream) {
+    int rc = check_w4(codes, scales, group, n_out, k_in);
+    if (rc) return rc;
+    if (!w || !aligned16(w)) return NOMAS_EINVAL;
+    DeviceScope dev(codes);
+    if (dev.rc) return dev.rc;
+    return enqueue_w4_dequant(codes, scales, group, n_out, k_in, w, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in) {
+    if (m <= kW4MaxRows || n_out < 1 || k_in < 1) return 0;
+    return (size_t)n_out * (size_t)k_in * 2;
+}
+
+extern "C" int nomas_w4a16_linear(const void *x, int64_t m, int64_t k_in, int64_t ldx, const uint8_t *codes,
+                                  const void *scales, int group, int64_t n_out, void *y, int64_t ldy, int y_dtype,
+                                  void *workspace, int32_t *status, nomas_stream stream) {
+    int rc = check_w4(codes, scales, group, n_out, k_in);
+    if (rc) return rc;
+    if (m < 0 || !x || !y || !status || !aligned16(x) || !aligned16(y) || !aligned16(status)) return NOMAS_EINVAL;
+    if (ldx < k_in || ldx % 8 != 0 || ldy < n_out) return NOMAS_EINVAL;
+    if (y_dtype != NOMAS_DTYPE_F32 && y_dtype != NOMAS_DTYPE_BF16) return NOMAS_EINVAL;
+    if (m >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
+    if (m > kW4MaxRows && (!workspace || !aligned16(workspace))) return NOMAS_EINVAL;
+    if (m == 0) return NOMAS_OK;
+    DeviceScope dev(codes);
+    if (dev.rc) return dev.rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (m > kW4MaxRows) {
+        rc = enqueue_w4_dequant(codes, scales, group, n_out, k_in, workspace, st);
+        if (rc) return rc;
+        return nomas_linear_bf16(x, m, k_in, ldx, workspace, n_out, k_in, y, ldy, y_dtype, status, stream);
+    }
+    W4Params p{};
+    p.codes = codes;
+    p.scales = static_cast<const __nv_bfloat16 *>(scales);
+    p.x = static_cast<const __nv_bfloat16 *>(x);
+    p.y = y;
+    p.ldx = ldx, p.ldy = ldy, p.n = n_out;
+    p.m = (int32_t)m, p.k = (int32_t)k_in;
+    p.groups = (int32_t)((k_in + group - 1) / group);
+    p.group_log2 = group_log2_of(group);
+    p.y_bf16 = y_dtype == NOMAS_DTYPE_BF16;
+    if (m <= 8) return launch_w4_rows<1>(p, st);
+    if (m <= 16) return launch_w4_rows<2>(p, st);
+    if (m <= 32) return launch_w4_rows<4>(p, st);
+    return launch_w4_rows<8>(p, st);
+}

@@ -1,7 +1,10 @@
 """Convenience wrapper over the C ABI: a KV cache whose device buffers are torch allocations.
 
+Next to it, the operators around the attention: rotary positions of q and k (AxisRope), layer norm with
+modulation (layer_norm, layer_norm_backward) and the linear layers with INT8 and 4-bit weights.
+
 Only allocation (torch), stream selection and argument marshalling happen here; the quantise-append,
-mask build and attention all run in libnomas's kernels.
+mask build, attention and these operators all run in libnomas's kernels.
 """
 from __future__ import annotations
 
@@ -22,6 +25,53 @@ def _bf16_strides(t: torch.Tensor) -> Tuple[int, int]:
     if t.dtype != torch.bfloat16 or t.dim() != 3 or t.stride(2) != 1:
         raise ValueError("expected a bf16 [tokens, heads, head_dim] tensor with contiguous head_dim")
     return t.stride(0), t.stride(1)
+
+
+_DTYPES = {torch.float32: N.NOMAS_DTYPE_F32, torch.bfloat16: N.NOMAS_DTYPE_BF16}
+
+
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _pitch(t: torch.Tensor) -> int:
+    """Row pitch of a matrix; a single row's own stride says nothing."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _token_strides(t: torch.Tensor) -> Tuple[int, int]:
+    """Token and head strides of [tokens, heads, head_dim]; a single token's or head's stride says nothing."""
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def _same_device(ref: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    for t in others:
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"tensors on {ref.device} and {t.device}: expected one device")
+
+
+class _on:
+    """Runs a call on the device of `ref`: its current stream, or `stream` (allocations then belong to it)."""
+
+    __slots__ = ("device", "stream", "guards")
+
+    def __init__(self, ref: torch.Tensor, stream: Optional[torch.cuda.Stream]):
+        if not ref.is_cuda:
+            raise ValueError(f"expected a CUDA tensor, got one on {ref.device}")
+        self.device, self.stream, self.guards = ref.device, stream, ()
+
+    def __enter__(self) -> int:
+        if self.stream is not None:
+            self.guards = (torch.cuda.stream(self.stream),)
+        elif self.device.index != torch.cuda.current_device():
+            self.guards = (torch.cuda.device(self.device),)
+        for g in self.guards:
+            g.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for g in self.guards:
+            g.__exit__(*exc)
 
 
 def segment_text(n_frames: int, head_len: int, tails: Sequence[Tuple[int, int, int]] = ()):
@@ -260,3 +310,215 @@ class Int8Linear:
 
     def status(self, stream=None) -> int:
         return N.nomas_status_read(self.status_word.data_ptr(), _stream_handle(stream))
+
+
+class Int4Linear:
+    """A linear layer with 4-bit weights and bf16 group scales, computed in BF16 (include/nomas.h): codes
+    uint8 [N][K / 2] (even column in the low half, stored + 8) and scales bf16 [N][ceil(K / group)] stay
+    resident.  Few rows of x read every code once and widen it in registers; more rows dequantise into a
+    transient bf16 workspace (allocated by the call) and run the tensor-core GEMM."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, group: int = 64):
+        if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous() or codes.shape[1] % 16:
+            raise ValueError("codes: contiguous uint8 [N, K / 2], K a multiple of 32")
+        self.n_out, self.k_in = codes.shape[0], 2 * codes.shape[1]
+        if group not in (32, 64, 128):
+            raise ValueError("group: 32, 64 or 128")
+        if scales.dtype != torch.bfloat16 or scales.shape != (self.n_out, -(-self.k_in // group)) or \
+                not scales.is_contiguous() or scales.device != codes.device:
+            raise ValueError("scales: contiguous bfloat16 [N, ceil(K / group)] on the device of codes")
+        self.codes, self.scales, self.group = codes, scales, group
+        self.status_word = torch.zeros(4, dtype=torch.int32, device=codes.device)
+
+    @classmethod
+    def from_weights(cls, w: torch.Tensor, group: int = 64, stream=None) -> "Int4Linear":
+        """Quantise bf16 weights [N, K] on the device."""
+        if w.dtype != torch.bfloat16 or w.dim() != 2 or w.stride(1) != 1 or w.shape[1] % 32 or group not in (32, 64, 128):
+            raise ValueError("w: bf16 [N, K] with contiguous rows, K a multiple of 32; group: 32, 64 or 128")
+        n, k = w.shape
+        with _on(w, stream) as st:
+            codes = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+            scales = torch.empty((n, -(-k // group)), dtype=torch.bfloat16, device=w.device)
+            N._check(N.nomas_w4_quantize(w.data_ptr(), n, k, w.stride(0), group, codes.data_ptr(), scales.data_ptr(),
+                                         st), "nomas_w4_quantize")
+            return cls(codes, scales, group)
+
+    def dequantized(self, stream=None) -> torch.Tensor:
+        with _on(self.codes, stream) as st:
+            w = torch.empty((self.n_out, self.k_in), dtype=torch.bfloat16, device=self.codes.device)
+            N._check(N.nomas_w4_dequant(self.codes.data_ptr(), self.scales.data_ptr(), self.group, self.n_out,
+                                        self.k_in, w.data_ptr(), st), "nomas_w4_dequant")
+        return w
+
+    def __call__(self, x: torch.Tensor, out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != self.k_in:
+            raise ValueError("x: bf16 [M, K] with contiguous rows")
+        m = x.shape[0]
+        if out is not None and (out.shape != (m, self.n_out) or out.dtype not in _DTYPES or out.stride(1) != 1):
+            raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
+        _same_device(self.codes, x, out)
+        with _on(self.codes, stream) as st:
+            if out is None:
+                out = torch.empty((m, self.n_out), dtype=out_dtype, device=x.device)
+            need = N.nomas_w4a16_workspace_bytes(m, self.n_out, self.k_in)
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+            if m:
+                N._check(N.nomas_w4a16_linear(x.data_ptr(), m, self.k_in, _pitch(x), self.codes.data_ptr(),
+                                              self.scales.data_ptr(), self.group, self.n_out, out.data_ptr(),
+                                              _pitch(out), _DTYPES[out.dtype], ws.data_ptr() if need else 0,
+                                              self.status_word.data_ptr(), st), "nomas_w4a16_linear")
+        return out
+
+    def status(self, stream=None) -> int:
+        with _on(self.codes, stream) as st:
+            return N.nomas_status_read(self.status_word.data_ptr(), st)
+
+
+# ------------------------------------------------------------------------------------------------
+# rotary positions
+# ------------------------------------------------------------------------------------------------
+
+def rope_grid(grid_h: int, grid_w: int, origin=(0.0, 0.0, 0.0), step=(1.0, 1.0, 1.0)) -> "N.nomas_rope_grid":
+    """Positions of video tokens in memory order: token n is frame n // (grid_h * grid_w), then row, then
+    column, at origin + step * index on the time, height and width axes."""
+    return N.make_rope_grid(grid_h, grid_w, tuple(origin), tuple(step))
+
+
+class AxisRope:
+    """Rotary positions over (time, height, width) for q and k (include/nomas.h).  axis_dims: channels of a
+    head that each axis turns; the channels behind them pass through."""
+
+    def __init__(self, head_dim: int, axis_dims: Sequence[int], theta: float = 10000.0, pairing: str = "interleaved"):
+        if pairing not in ("interleaved", "halves"):
+            raise ValueError("pairing: 'interleaved' or 'halves'")
+        if len(axis_dims) != 3:
+            raise ValueError("axis_dims: channels of time, height and width")
+        self.head_dim = head_dim
+        self.spec = N.make_rope_spec(head_dim, axis_dims, theta,
+                                     N.NOMAS_ROPE_HALVES if pairing == "halves" else N.NOMAS_ROPE_INTERLEAVED)
+
+    def __call__(self, tensors, grid=None, positions: Optional[torch.Tensor] = None, inverse: bool = False, out=None,
+                 stream=None):
+        """Rotate one [tokens, heads, head_dim] tensor (bf16 or fp32) or a sequence of them (q and k: one
+        launch), at the positions of `grid` (rope_grid) or `positions` (fp32 [tokens, 3]).  inverse: the
+        inverse rotation, which is also the gradient.  out: tensors to write (x itself: in place)."""
+        single = isinstance(tensors, torch.Tensor)
+        xs = (tensors,) if single else tuple(tensors)
+        if not 1 <= len(xs) <= N.NOMAS_ROPE_MAX_TENSORS:
+            raise ValueError(f"1 to {N.NOMAS_ROPE_MAX_TENSORS} tensors")
+        ref = xs[0]
+        if ref.dim() != 3 or ref.dtype not in _DTYPES:
+            raise ValueError("expected bf16 or fp32 [tokens, heads, head_dim] tensors with contiguous head_dim")
+        if (grid is None) == (positions is None):
+            raise ValueError("give either grid or positions")
+        t = ref.shape[0]
+        if positions is not None and (positions.dtype != torch.float32 or positions.shape != (t, 3) or
+                                      not positions.is_contiguous()):
+            raise ValueError("positions: contiguous fp32 [tokens, 3]")
+        with _on(ref, stream) as st:
+            if out is None:
+                ys = tuple(torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs)
+            else:
+                ys = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+                if len(ys) != len(xs):
+                    raise ValueError("out: one tensor for each input")
+            _same_device(ref, positions, *xs, *ys)
+            args = []
+            for x, y in zip(xs, ys):
+                for v in (x, y):
+                    if v.dtype != ref.dtype or v.dim() != 3 or v.shape[0] != t or v.shape[2] != self.head_dim or \
+                            v.shape[1] != x.shape[1] or v.stride(2) != 1:
+                        raise ValueError("expected tensors [tokens, heads, head_dim] of one type and token count with "
+                                         "contiguous head_dim")
+                args.append((x.data_ptr(), y.data_ptr(), *_token_strides(x), *_token_strides(y), x.shape[1]))
+            if t and all(a[-1] for a in args):
+                N._check(N.nomas_rope(self.spec, grid, positions.data_ptr() if positions is not None else 0, t,
+                                      N.make_rope_tensors(args), len(args), _DTYPES[ref.dtype], inverse, st), "nomas_rope")
+        return ys[0] if single else ys
+
+
+# ------------------------------------------------------------------------------------------------
+# layer norm
+# ------------------------------------------------------------------------------------------------
+
+def _norm_params(x, weight, bias, rows_per_group):
+    """(weight, bias, pitch, type, groups) of a layer norm's parameters: [C], or [groups, C]."""
+    if x.dim() != 2 or x.dtype not in _DTYPES or x.stride(1) != 1:
+        raise ValueError("x: bf16 or fp32 [rows, C] with contiguous rows")
+    rows, cols = x.shape
+    groups = -(-rows // rows_per_group) if rows_per_group else 1
+    dtype, pitch = None, None
+    for name, p in (("weight", weight), ("bias", bias)):
+        if p is None:
+            continue
+        if p.dtype not in _DTYPES or p.shape not in (((cols,), (1, cols)) if groups == 1 else ((groups, cols),)) or \
+                p.stride(-1) != 1:
+            raise ValueError(f"{name}: bf16 or fp32 [groups, C] ([C] for one group) with contiguous rows")
+        at = p.stride(0) if p.dim() == 2 and groups > 1 else cols
+        if pitch is not None and (at != pitch or p.dtype != dtype):
+            raise ValueError("weight and bias must share their type and strides")
+        dtype, pitch = p.dtype, at
+    return pitch or cols, _DTYPES[dtype] if dtype is not None else N.NOMAS_DTYPE_F32, groups
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-6, rows_per_group: int = 0, unit_offset: bool = False, out_dtype=None,
+               out: Optional[torch.Tensor] = None, want_stats: bool = False, stream=None):
+    """Layer norm of the rows of x [rows, C] (include/nomas.h): xhat * weight + bias, or with unit_offset
+    xhat * (1 + weight) + bias (modulation).  rows_per_group: rows that share a row of weight and bias
+    ([groups, C]); 0: one weight and bias [C] for all.  Returns y, or (y, mean, rstd) with want_stats, which
+    layer_norm_backward takes."""
+    if rows_per_group < 0:
+        raise ValueError("rows_per_group: at least 0")
+    pitch, p_dtype, _ = _norm_params(x, weight, bias, rows_per_group)
+    rows, cols = x.shape
+    if out is not None and (out.shape != x.shape or out.dtype not in _DTYPES or out.stride(1) != 1):
+        raise ValueError("out: bf16 or fp32 [rows, C] with contiguous rows")
+    _same_device(x, weight, bias, out)
+    with _on(x, stream) as st:
+        if out is None:
+            out = torch.empty((rows, cols), dtype=out_dtype or x.dtype, device=x.device)
+        mean = rstd = None
+        if want_stats:
+            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if rows:
+            N._check(N.nomas_layernorm_fwd(x.data_ptr(), rows, cols, _pitch(x), _DTYPES[x.dtype], _ptr(weight), _ptr(bias),
+                                           pitch, p_dtype, rows_per_group, unit_offset, eps, out.data_ptr(), _pitch(out),
+                                           _DTYPES[out.dtype], _ptr(mean), _ptr(rstd), st), "nomas_layernorm_fwd")
+    return (out, mean, rstd) if want_stats else out
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: Optional[torch.Tensor] = None, rows_per_group: int = 0, unit_offset: bool = False,
+                        want_dx: bool = True, want_params: bool = True, stream=None):
+    """Gradients of layer_norm: (dx of x's type, dweight fp32 [groups, C], dbias fp32 [groups, C]); what is not
+    wanted is None.  mean and rstd are layer_norm's."""
+    if rows_per_group < 0:
+        raise ValueError("rows_per_group: at least 0")
+    pitch, p_dtype, groups = _norm_params(x, weight, None, rows_per_group)
+    rows, cols = x.shape
+    if dy.shape != x.shape or dy.dtype not in _DTYPES or dy.stride(1) != 1:
+        raise ValueError("dy: bf16 or fp32 [rows, C] with contiguous rows")
+    for s in (mean, rstd):
+        if s.dtype != torch.float32 or s.shape != (rows,) or not s.is_contiguous():
+            raise ValueError("mean, rstd: contiguous fp32 [rows]")
+    _same_device(x, dy, mean, rstd, weight)
+    with _on(x, stream) as st:
+        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if want_dx else None
+        dw = db = ws = None
+        if want_params:
+            dw = torch.empty((groups, cols), dtype=torch.float32, device=x.device)
+            db = torch.empty((groups, cols), dtype=torch.float32, device=x.device)
+            ws = torch.empty(N.nomas_layernorm_workspace_bytes(rows, cols, rows_per_group), dtype=torch.uint8,
+                             device=x.device)
+        if rows and (want_dx or want_params):
+            N._check(N.nomas_layernorm_bwd(dy.data_ptr(), _pitch(dy), _DTYPES[dy.dtype], x.data_ptr(), _pitch(x),
+                                           _DTYPES[x.dtype], rows, cols, _ptr(weight), pitch, p_dtype, rows_per_group,
+                                           unit_offset, mean.data_ptr(), rstd.data_ptr(), _ptr(dx), cols, _ptr(dw),
+                                           _ptr(db), cols, _ptr(ws), st), "nomas_layernorm_bwd")
+        elif want_params:
+            dw.zero_()
+            db.zero_()
+    return dx, dw, db
