@@ -5,11 +5,16 @@
 // x and writes dx, about 8 and 14 flops a value.  A row stays in the registers of a team of threads (a
 // power of two), so that the variance is a second sum over registers (exact differences, no sum of squares
 // that cancels) and memory is read once.
-//   layernorm_fwd_kernel   one row per team
-//   layernorm_bwd_kernel   a CTA takes a contiguous share of the rows, R rows of each team at a time; a
-//                          thread owns columns, so dw and db of a group add up in its registers in row
-//                          order.  Groups inside a share are written at once; where a group goes on in
-//                          the next share, its sums so far go to the workspace (two slots a CTA).
+//   layernorm_row_kernel   forward, one row per team, loads straight into registers: few rows (latency),
+//                          and layouts that allow no wide loads
+//   layernorm_fwd_kernel   forward, a CTA takes a contiguous share of the rows.  Every thread keeps its own
+//                          ring of 16-byte chunks in shared memory, filled by asynchronous copies several rows
+//                          ahead (nothing to synchronise: a thread reads what it copied), and the group's
+//                          weight and bias rows wait in shared memory too.
+//   layernorm_bwd_kernel   a CTA takes a contiguous share of the rows, R rows of each team at a time, through
+//                          the same rings; a thread owns columns, so dw and db of a group add up in its
+//                          registers in row order.  Groups inside a share are written at once; where a group
+//                          goes on in the next share, its sums so far go to the workspace (two slots a CTA).
 //   layernorm_grad_kernel  adds up the shares of such groups, in share order.
 #include "common.cuh"
 
@@ -27,6 +32,8 @@ struct NormParams {
     int32_t team_log2;          // log2(threads of a team)
     int32_t p_bf16;
     float unit, eps;
+    uint32_t share;             // rows of a CTA (layernorm_fwd_kernel)
+    int32_t in_smem;            // it keeps the group's parameters in shared memory
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -93,57 +100,79 @@ __device__ __forceinline__ void load_param(const void *base, int32_t bf16, int64
         load_chunk<CH>(static_cast<const float *>(base) + at, v);
 }
 
-// Sum of N values over a team of 2^log2 threads; every thread gets it, in an order that depends on the
-// team alone.  Teams of more than a warp meet in `red` (N floats per warp and parity); all threads of the
-// CTA call it equally often.
+// Sums of N values (N = 1, 2, 4, 8) over a team of 2^log2 threads; every thread gets them, in an order that
+// depends on the team alone.  In a warp the N values are halved between the lanes as they are added up (N - 1
+// + log2(32 / N) shuffles, not 5 N).  Teams of more than a warp meet in `red` (N floats per warp of the CTA and
+// parity) at a barrier of their own; a team's threads call it equally often.
 template <int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], int log2, float *red, int &parity) {
+    const int lane = threadIdx.x & 31;
+    if (log2 < 5) {
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        if (off >> log2) break;
+        for (int off = 1; off < 16; off <<= 1) {
+            if (off >> log2) break;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+        }
+        return;
     }
-    if (log2 <= 5) return;
-    const int warp = threadIdx.x >> 5, warps = 1 << (log2 - 5), first = warp & ~(warps - 1);
-    float *r = red + parity * (int)(blockDim.x >> 5) * N;
-    parity ^= 1;                // the next sum's writes do not meet this one's reads
-    if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) r[warp * N + i] = v[i];
+    for (int n = N / 2, off = 16; n >= 1; n >>= 1, off >>= 1) {
+        const bool upper = lane & off;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+        }
     }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    for (int k = 0; k < warps; ++k) {
+    for (int off = 16 / N; off >= 1; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    // value i is in the lanes 32 / N * i ..
+    float s = v[0];
+    int step = 32 / N;
+    if (log2 > 5) {
+        const int warp = threadIdx.x >> 5, warps = 1 << (log2 - 5), first = warp & ~(warps - 1);
+        float *r = red + parity * (int)(blockDim.x >> 5) * N;
+        parity ^= 1;            // the next sum's writes do not meet this one's reads
+        if (lane % step == 0) r[warp * N + lane / step] = s;
+        named_bar_sync(1 + (int)(threadIdx.x >> log2), 1 << log2);
+        s = 0.0f;
+        for (int e = lane; e < warps * N; e += 32) s += r[first * N + e];
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += r[(first + k) * N + i];
+        for (int off = 16; off >= N; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        step = 1;
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, s, i * step);
 }
 
-template <typename TX, typename TY, int CH, int NV>
-__global__ void __launch_bounds__(kNormThreads) layernorm_fwd_kernel(const NormParams p) {
-    __shared__ float red[2 * kNormThreads / 32];
-    const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1);
-    const int64_t row = ((int64_t)blockIdx.x * kNormThreads + threadIdx.x) >> p.team_log2;
-    const bool live = row < p.rows;
-    const TX *x = static_cast<const TX *>(p.x) + row * p.ldx;
-    float v[NV][CH];
-    int parity = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const uint32_t c = (uint32_t)(lane + j * team) * CH;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) v[j][i] = 0.0f;
-        if (live && c < p.cols) load_chunk<CH>(x + c, v[j]);
-    }
+// Asynchronous copy of a chunk of BYTES (8 or 16) into shared memory, in the groups that ring_commit closes.
+template <int BYTES>
+__device__ __forceinline__ void ring_load(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of this thread have landed.
+template <int N>
+__device__ __forceinline__ void ring_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Mean and 1 / sqrt(variance + eps) of the row in v; v becomes x - mean.
+template <int CH, int NV>
+__device__ __forceinline__ float centre_row(float (&v)[NV][CH], int lane, const NormParams &p, float *red, int &parity,
+                                            float &mean) {
+    const int team = 1 << p.team_log2;
     float s[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < CH; ++i) s[0] += v[j][i];
     team_sum<1>(s, p.team_log2, red, parity);
-    const float mean = s[0] / (float)p.cols;
+    mean = s[0] / (float)p.cols;
     s[0] = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -155,27 +184,142 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_fwd_kernel(const NormP
         }
     }
     team_sum<1>(s, p.team_log2, red, parity);
-    const float rstd = 1.0f / sqrtf(s[0] / (float)p.cols + p.eps);
+    return 1.0f / sqrtf(s[0] / (float)p.cols + p.eps);
+}
+
+template <typename TX, typename TY, int CH, int NV>
+__global__ void __launch_bounds__(kNormThreads) layernorm_row_kernel(const NormParams p) {
+    __shared__ float red[2 * kNormThreads / 32];
+    const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1);
+    const int64_t row = ((int64_t)blockIdx.x * kNormThreads + threadIdx.x) >> p.team_log2;
+    const bool live = row < p.rows;
+    const TX *x = static_cast<const TX *>(p.x) + row * p.ldx;
+    const int64_t pg = live ? (int64_t)fdiv((uint32_t)row, p.group) * p.ldp : 0;
+    float v[NV][CH], w[NV][CH], b[NV][CH];
+    int parity = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const uint32_t c = (uint32_t)(lane + j * team) * CH;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) v[j][i] = b[j][i] = 0.0f, w[j][i] = 1.0f - p.unit;
+        if (!live || c >= p.cols) continue;
+        load_chunk<CH>(x + c, v[j]);
+        if (p.w) load_param<CH>(p.w, p.p_bf16, pg + c, w[j]);
+        if (p.b) load_param<CH>(p.b, p.p_bf16, pg + c, b[j]);
+    }
+    float mean;
+    const float rstd = centre_row<CH, NV>(v, lane, p, red, parity, mean);
     if (!live) return;
     if (lane == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
-    const int64_t pg = (int64_t)fdiv((uint32_t)row, p.group) * p.ldp;
     TY *y = static_cast<TY *>(p.y) + row * p.ldy;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const uint32_t c = (uint32_t)(lane + j * team) * CH;
         if (c >= p.cols) continue;
-        float w[CH], b[CH];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) w[i] = 1.0f - p.unit, b[i] = 0.0f;
-        if (p.w) load_param<CH>(p.w, p.p_bf16, pg + c, w);
-        if (p.b) load_param<CH>(p.b, p.p_bf16, pg + c, b);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) w[i] = fmaf(v[j][i] * rstd, p.unit + w[i], b[i]);
-        store_chunk<CH>(y + c, w);
+        for (int i = 0; i < CH; ++i) v[j][i] = fmaf(v[j][i] * rstd, p.unit + w[j][i], b[j][i]);
+        store_chunk<CH>(y + c, v[j]);
     }
+}
+
+// Stages of the forward ring: about 256 bytes a thread in flight.
+template <int NV>
+struct FwdRing {
+    static constexpr int kStages = NV >= 8 ? 3 : NV == 4 ? 5 : 8;
+};
+
+template <typename TX, typename TY, int CH, int NV>
+__global__ void __launch_bounds__(kNormThreads, NV * CH > 32 ? 2 : 3) layernorm_fwd_kernel(const NormParams p) {
+    constexpr int S = FwdRing<NV>::kStages, BYTES = CH * sizeof(TX);
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float red[2 * kNormThreads / 32];
+    const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), mine = threadIdx.x >> p.team_log2;
+    const uint32_t teams = kNormThreads >> p.team_log2;
+    const uint32_t begin = blockIdx.x * p.share, end = min(p.rows, begin + p.share);
+    const uint32_t ring = smem_u32(smem) + threadIdx.x * BYTES;
+    const uint8_t *ring_at = smem + threadIdx.x * BYTES;
+    uint8_t *params = smem + S * NV * kNormThreads * BYTES;
+    const int64_t psize = p.p_bf16 ? 2 : 4;
+    int parity = 0;
+    // the rounds of the share in order: `teams` rows from fetch_row, inside a run of rows that share parameters
+    // (the whole share when they are read from global memory: groups of few rows, or rows too wide)
+    uint32_t fetch_row = begin, fetch_stop = begin;
+    auto run_end = [&](uint32_t row) {
+        return p.in_smem ? (uint32_t)min((int64_t)end, ((int64_t)fdiv(row, p.group) + 1) * p.group.d) : end;
+    };
+    auto fetch = [&](int stage) {
+        if (fetch_row < end) {
+            if (fetch_row >= fetch_stop) fetch_stop = run_end(fetch_row);
+            const uint32_t at = fetch_row + mine;
+            const TX *x = static_cast<const TX *>(p.x) + (int64_t)at * p.ldx;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const uint32_t c = (uint32_t)(lane + j * team) * CH;
+                if (at < fetch_stop && c < p.cols) ring_load<BYTES>(ring + (stage * NV + j) * kNormThreads * BYTES, x + c);
+            }
+            fetch_row = min(fetch_row + teams, fetch_stop);
+        }
+        ring_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) fetch(k);
+    int stage = 0, last = S - 1;
+    for (uint32_t row = begin; row < end;) {
+        const uint32_t stop = run_end(row);
+        if (p.in_smem) {
+            const int64_t from = (int64_t)fdiv(row, p.group) * p.ldp * psize, bytes = (int64_t)p.cols * psize;
+            __syncthreads();
+            for (int64_t o = threadIdx.x * 16; o < bytes; o += kNormThreads * 16) {
+                if (p.w) *reinterpret_cast<uint4 *>(params + o) = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.w) + from + o);
+                if (p.b) *reinterpret_cast<uint4 *>(params + bytes + o) = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.b) + from + o);
+            }
+            __syncthreads();
+        }
+        for (uint32_t r0 = row; r0 < stop; r0 += teams) {
+            const uint32_t at = r0 + mine;
+            const bool live = at < stop;        // every thread takes part in the sums
+            fetch(last);
+            ring_wait<S - 1>();
+            float v[NV][CH];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const uint32_t c = (uint32_t)(lane + j * team) * CH;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) v[j][i] = 0.0f;
+                if (live && c < p.cols) load_chunk<CH>(reinterpret_cast<const TX *>(ring_at + (stage * NV + j) * kNormThreads * BYTES), v[j]);
+            }
+            last = stage;
+            stage = stage + 1 == S ? 0 : stage + 1;
+            float mean;
+            const float rstd = centre_row<CH, NV>(v, lane, p, red, parity, mean);
+            if (!live) continue;
+            if (lane == 0) {
+                if (p.mean) p.mean[at] = mean;
+                if (p.rstd) p.rstd[at] = rstd;
+            }
+            const void *wr = p.in_smem ? params : p.w, *br = p.in_smem ? params + p.cols * psize : p.b;
+            const int64_t pg = p.in_smem ? 0 : (int64_t)fdiv(at, p.group) * p.ldp;
+            TY *y = static_cast<TY *>(p.y) + (int64_t)at * p.ldy;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const uint32_t c = (uint32_t)(lane + j * team) * CH;
+                if (c >= p.cols) continue;
+                float w[CH], b[CH];
+#pragma unroll
+                for (int i = 0; i < CH; ++i) w[i] = 1.0f - p.unit, b[i] = 0.0f;
+                if (p.w) load_param<CH>(wr, p.p_bf16, pg + c, w);
+                if (p.b) load_param<CH>(br, p.p_bf16, pg + c, b);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) v[j][i] = fmaf(v[j][i] * rstd, p.unit + w[i], b[i]);
+                store_chunk<CH>(y + c, v[j]);
+            }
+        }
+        row = stop;
+    }
+    ring_wait<0>();
 }
 
 struct NormBwdParams {
@@ -185,36 +329,32 @@ struct NormBwdParams {
     float *dw, *db, *part;      // part: [CTAs][2][2][cols] (share, head or tail of it, dw or db)
     int64_t lddy, ldx, lddx, ldp, ldg;
     uint32_t rows, cols, share; // share: rows of a CTA
+    int32_t by_group;           // layernorm_grad_kernel: a grid row is a group
     FastDiv group;
-    int32_t team_log2, p_bf16;
+    int32_t team_log2, p_bf16, grad_wide;       // grad_wide: rows of dw and db take 16-byte stores
     float unit;
 };
 
 // dw and db of a group (or of a part of one) from the CTA's threads: teams of the CTA hold the same columns.
 template <int CH, int NV, int T>
 __device__ __forceinline__ void flush_grads(const NormBwdParams &p, float (&aw)[NV][CH], float (&ab)[NV][CH], float *dw,
-                                            float *db, float *meet) {
+                                            float *db, bool wide, float *meet) {
     const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), teams = T >> p.team_log2;
     if (NV == 1 && teams > 1) { // a larger NV has one team
-        const int stride = team * CH * NV, mine = threadIdx.x >> p.team_log2;
+        const int stride = team * CH, mine = threadIdx.x >> p.team_log2;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int i = 0; i < CH; ++i)
-                    meet[mine * stride + (j * CH + i) * team + lane] = g ? ab[j][i] : aw[j][i];
+            for (int i = 0; i < CH; ++i) meet[mine * stride + i * team + lane] = g ? ab[0][i] : aw[0][i];
             __syncthreads();
             if (mine == 0) {
 #pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        float s = 0.0f;
-                        for (int k = 0; k < teams; ++k) s += meet[k * stride + (j * CH + i) * team + lane];
-                        (g ? ab[j][i] : aw[j][i]) = s;
-                    }
+                for (int i = 0; i < CH; ++i) {
+                    float s = 0.0f;
+                    for (int k = 0; k < teams; ++k) s += meet[k * stride + i * team + lane];
+                    (g ? ab[0][i] : aw[0][i]) = s;
+                }
             }
         }
     }
@@ -223,11 +363,15 @@ __device__ __forceinline__ void flush_grads(const NormBwdParams &p, float (&aw)[
         for (int j = 0; j < NV; ++j) {
             const uint32_t c = (uint32_t)(lane + j * team) * CH;
             if (c >= p.cols) continue;
-            // gradient rows of any pitch: element stores
+            if (CH > 1 && wide) {
+                if (dw) store_chunk<CH>(dw + c, aw[j]);
+                if (db) store_chunk<CH>(db + c, ab[j]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                if (dw) dw[c + i] = aw[j][i];
-                if (db) db[c + i] = ab[j][i];
+                for (int i = 0; i < CH; ++i) {
+                    if (dw) dw[c + i] = aw[j][i];
+                    if (db) db[c + i] = ab[j][i];
+                }
             }
         }
     }
@@ -237,8 +381,21 @@ __device__ __forceinline__ void flush_grads(const NormBwdParams &p, float (&aw)[
         for (int i = 0; i < CH; ++i) aw[j][i] = ab[j][i] = 0.0f;
 }
 
+// Backward ring: stages of R rows of x and dy, up to three in about 200 KB; without two (rows above 8192 columns
+// in fp32), and in narrow layouts (no copies of 8 bytes and more), rows are loaded straight into registers.
 template <typename TX, typename TY, int CH, int NV, int R, int T>
-__global__ void __launch_bounds__(T) layernorm_bwd_kernel(const NormBwdParams p) {
+struct BwdRing {
+    static constexpr int kStage = R * NV * CH * (int)(sizeof(TX) + sizeof(TY)) * T;
+    static constexpr int kFit = 200 * 1024 / kStage;
+    static constexpr int kStages = CH == 1 || kFit < 2 ? 0 : kFit < 3 ? kFit : 3;
+    static constexpr int kBytes = kStages * kStage;
+};
+
+template <typename TX, typename TY, int CH, int NV, int R, int T>
+__global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwdParams p) {
+    constexpr bool RING = BwdRing<TX, TY, CH, NV, R, T>::kStages > 0;
+    constexpr int S = RING ? BwdRing<TX, TY, CH, NV, R, T>::kStages : 1, XB = CH * sizeof(TX), YB = CH * sizeof(TY);
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2 * (T / 32) * 2 * R];
     __shared__ float meet[NV == 1 ? T * CH : 1];
     const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), mine = threadIdx.x >> p.team_log2;
@@ -251,13 +408,64 @@ __global__ void __launch_bounds__(T) layernorm_bwd_kernel(const NormBwdParams p)
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < CH; ++i) aw[j][i] = ab[j][i] = 0.0f;
+
+    // the batches of the share in order: R * teams rows from fetch_row, inside the group that ends at fetch_stop
+    uint32_t fetch_row = begin, fetch_stop = begin;
+    const uint8_t *ring_x = smem + threadIdx.x * XB, *ring_y = smem + S * R * NV * T * XB + threadIdx.x * YB;
+    auto fetch = [&](int stage) {
+        if (fetch_row < end) {
+            if (fetch_row >= fetch_stop)
+                fetch_stop = (uint32_t)min((int64_t)end, ((int64_t)fdiv(fetch_row, p.group) + 1) * p.group.d);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t at = fetch_row + r * teams + mine;
+                if (at >= fetch_stop) continue;
+                const TX *x = static_cast<const TX *>(p.x) + (int64_t)at * p.ldx;
+                const TY *dy = static_cast<const TY *>(p.dy) + (int64_t)at * p.lddy;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const uint32_t c = (uint32_t)(lane + j * team) * CH;
+                    if (c >= p.cols) continue;
+                    const int slot = (stage * R + r) * NV + j;
+                    ring_load<RING ? XB : 16>(smem_u32(ring_x + slot * T * XB), x + c);
+                    ring_load<RING ? YB : 16>(smem_u32(ring_y + slot * T * YB), dy + c);
+                }
+            }
+            fetch_row = min(fetch_row + R * teams, fetch_stop);
+        }
+        ring_commit();
+    };
+    int stage = 0, last = S - 1;
+    if constexpr (RING) {
+#pragma unroll
+        for (int k = 0; k < S - 1; ++k) fetch(k);
+    }
     for (uint32_t row = begin; row < end;) {
         const uint32_t g = fdiv(row, p.group);
         const int64_t g0 = (int64_t)g * p.group.d, g1 = min(g0 + (int64_t)p.group.d, (int64_t)p.rows);
         const uint32_t stop = (uint32_t)min((int64_t)end, g1);
-        const int64_t pg = (int64_t)g * p.ldp;
+        float f[NV][CH];                        // u + w
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t c = (uint32_t)(lane + j * team) * CH;
+#pragma unroll
+            for (int i = 0; i < CH; ++i) f[j][i] = 1.0f - p.unit;
+            if (p.w && c < p.cols) load_param<CH>(p.w, p.p_bf16, (int64_t)g * p.ldp + c, f[j]);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) f[j][i] += p.unit;
+        }
         for (uint32_t r0 = row; r0 < stop; r0 += teams * R) {
-            float xh[R][NV][CH], gy[R][NV][CH], s[2 * R], rstd[R];
+            float mean[R], rstd[R], xh[R][NV][CH], gy[R][NV][CH], s[2 * R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t at = r0 + r * teams + mine;
+                mean[r] = at < stop ? __ldg(p.mean + at) : 0.0f;
+                rstd[r] = at < stop ? __ldg(p.rstd + at) : 0.0f;
+            }
+            if constexpr (RING) {
+                fetch(last);
+                ring_wait<S - 1>();
+            }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const uint32_t at = r0 + r * teams + mine;
@@ -269,33 +477,31 @@ __global__ void __launch_bounds__(T) layernorm_bwd_kernel(const NormBwdParams p)
                     const uint32_t c = (uint32_t)(lane + j * team) * CH;
 #pragma unroll
                     for (int i = 0; i < CH; ++i) xh[r][j][i] = gy[r][j][i] = 0.0f;
-                    if (live && c < p.cols) {
+                    if (!live || c >= p.cols) continue;
+                    if constexpr (RING) {
+                        const int slot = (stage * R + r) * NV + j;
+                        load_chunk<CH>(reinterpret_cast<const TX *>(ring_x + slot * T * XB), xh[r][j]);
+                        load_chunk<CH>(reinterpret_cast<const TY *>(ring_y + slot * T * YB), gy[r][j]);
+                    } else {
                         load_chunk<CH>(x + c, xh[r][j]);
                         load_chunk<CH>(dy + c, gy[r][j]);
                     }
                 }
             }
+            last = stage;
+            stage = stage + 1 == S ? 0 : stage + 1;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const uint32_t at = r0 + r * teams + mine;
-                const bool live = at < stop;
-                const float mean = live ? __ldg(p.mean + at) : 0.0f;
-                rstd[r] = live ? __ldg(p.rstd + at) : 0.0f;
                 s[2 * r] = s[2 * r + 1] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const uint32_t c = (uint32_t)(lane + j * team) * CH;
-                    if (!live || c >= p.cols) continue;
-                    float w[CH];
-#pragma unroll
-                    for (int i = 0; i < CH; ++i) w[i] = 1.0f - p.unit;
-                    if (p.w) load_param<CH>(p.w, p.p_bf16, pg + c, w);
+                    const bool in = (uint32_t)(lane + j * team) * CH < p.cols;
 #pragma unroll
                     for (int i = 0; i < CH; ++i) {
-                        const float xv = (xh[r][j][i] - mean) * rstd[r], d = gy[r][j][i];
+                        const float xv = in ? (xh[r][j][i] - mean[r]) * rstd[r] : 0.0f, d = gy[r][j][i];
                         aw[j][i] = fmaf(d, xv, aw[j][i]);
                         ab[j][i] += d;
-                        const float gv = d * (p.unit + w[i]);
+                        const float gv = d * f[j][i];
                         s[2 * r] += gv;
                         s[2 * r + 1] = fmaf(gv, xv, s[2 * r + 1]);
                         xh[r][j][i] = xv;
@@ -323,44 +529,49 @@ __global__ void __launch_bounds__(T) layernorm_bwd_kernel(const NormBwdParams p)
         }
         if (p.dw || p.db) {
             float *dw, *db;
+            bool wide = true;
             if (g0 >= begin && g1 <= end) {
                 dw = p.dw ? p.dw + (int64_t)g * p.ldg : nullptr;
                 db = p.db ? p.db + (int64_t)g * p.ldg : nullptr;
+                wide = p.grad_wide;
             } else {            // slot 0: the group began in an earlier share, 1: it goes on in a later one
                 dw = p.part + ((int64_t)blockIdx.x * 2 + (g0 < begin ? 0 : 1)) * 2 * p.cols;
                 db = dw + p.cols;
             }
-            flush_grads<CH, NV, T>(p, aw, ab, dw, db, meet);
+            flush_grads<CH, NV, T>(p, aw, ab, dw, db, wide, meet);
         }
         row = stop;
     }
+    if constexpr (RING) ring_wait<0>();
 }
 
-// Groups that several shares hold: the CTAs of row y of the grid add up the group that begins in share y
-// and goes on behind it, if there is one.  32 columns of dw or of db a CTA, kGradRows shares at a time.
-constexpr int kGradRows = 16;
+// Groups that several shares hold.  Row y of the grid is group y, or with more groups than shares the group
+// that begins in share y and goes on behind it, if there is one.  32 columns of dw or of db a CTA, kGradRows
+// shares at a time.
+constexpr int kGradRows = 8;
 
 __global__ void __launch_bounds__(32 * kGradRows) layernorm_grad_kernel(const NormBwdParams p) {
     __shared__ float red[kGradRows][33];
     griddep_wait();
-    const int64_t begin = (int64_t)blockIdx.y * p.share, end = min((int64_t)p.rows, begin + p.share);
-    const uint32_t g = fdiv((uint32_t)(end - 1), p.group);
-    const int64_t g0 = (int64_t)g * p.group.d, g1 = min(g0 + (int64_t)p.group.d, (int64_t)p.rows);
-    if (g0 < begin || g1 <= end) return;
+    const int64_t g = p.by_group ? blockIdx.y : fdiv((uint32_t)min((int64_t)p.rows, ((int64_t)blockIdx.y + 1) * p.share) - 1, p.group);
+    const int64_t g0 = g * p.group.d, g1 = min(g0 + (int64_t)p.group.d, (int64_t)p.rows);
+    const int64_t first = g0 / p.share, final = (g1 - 1) / p.share;
+    if (first == final || (!p.by_group && first != blockIdx.y)) return;
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int64_t at = (int64_t)blockIdx.x * 32 + lane;         // 0 .. 2 cols - 1: dw then db
-    const int64_t last = (g1 - 1) / p.share;
     float s = 0.0f;
-    if (at < 2 * (int64_t)p.cols)
-        for (int64_t b = blockIdx.y + k; b <= last; b += kGradRows)
-            s += p.part[(b * 2 + (b == blockIdx.y ? 1 : 0)) * 2 * p.cols + at];
+    if (at < 2 * (int64_t)p.cols) {
+        const float *part = p.part + at;
+#pragma unroll 4
+        for (int64_t b = first + k; b <= final; b += kGradRows) s += part[(b * 2 + (b == first ? 1 : 0)) * 2 * p.cols];
+    }
     red[k][lane] = s;
     __syncthreads();
     if (k != 0 || at >= 2 * (int64_t)p.cols) return;
 #pragma unroll
     for (int i = 1; i < kGradRows; ++i) s += red[i][lane];
     float *out = at < p.cols ? p.dw : p.db;
-    if (out) out[(int64_t)g * p.ldg + (at < p.cols ? at : at - p.cols)] = s;
+    if (out) out[g * p.ldg + (at < p.cols ? at : at - p.cols)] = s;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -404,34 +615,71 @@ static int team_of(int64_t chunks, int per, int most) {
     return l > most ? most : l;
 }
 
+// Dynamic shared memory above 48 KB has to be allowed per kernel and device.
+static int allow_smem(const void *kernel, int bytes) {
+    if (bytes <= 48 * 1024) return NOMAS_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return e == cudaSuccess ? NOMAS_OK : cuda_fail("cudaFuncSetAttribute(layer norm smem)", (int)e, cudaGetErrorString(e));
+}
+
 template <typename TX, typename TY, int CH, int NV>
-static int launch_fwd(const NormParams &p, cudaStream_t st) {
+static int launch_row(const NormParams &p, cudaStream_t st) {
     const int64_t threads = (int64_t)p.rows << p.team_log2;
-    layernorm_fwd_kernel<TX, TY, CH, NV>
+    layernorm_row_kernel<TX, TY, CH, NV>
         <<<(unsigned)((threads + kNormThreads - 1) / kNormThreads), kNormThreads, 0, st>>>(p);
+    return check_launch("layernorm_row_kernel launch");
+}
+
+// The row's loads spread over as many threads as a CTA has.
+template <typename TX, typename TY, int CH>
+static int pick_row(NormParams &p, cudaStream_t st) {
+    const int64_t chunks = (p.cols + CH - 1) / CH;
+    p.team_log2 = team_of(chunks, 1, 8);
+    const int64_t nv = (chunks + (1 << p.team_log2) - 1) >> p.team_log2;
+    if (nv <= 1) return launch_row<TX, TY, CH, 1>(p, st);
+    if (nv <= 4) return launch_row<TX, TY, CH, 4>(p, st);
+    if (CH == 8 || nv <= 8) return launch_row<TX, TY, CH, 8>(p, st);
+    if (CH == 4 || nv <= 16) return launch_row<TX, TY, CH, CH == 8 ? 8 : 16>(p, st);
+    return launch_row<TX, TY, CH, CH == 1 ? 64 : 8>(p, st);
+}
+
+template <typename TX, typename TY, int CH, int NV>
+static int launch_fwd(NormParams &p, cudaStream_t st) {
+    constexpr int kRing = FwdRing<NV>::kStages * NV * CH * (int)sizeof(TX) * kNormThreads;
+    const int64_t row = 2 * (int64_t)p.cols * (p.p_bf16 ? 2 : 4);
+    // a group's parameters are loaded once a CTA: worth it from a few rounds of rows on
+    const int64_t teams = kNormThreads >> p.team_log2;
+    p.in_smem = (p.w || p.b) && row <= 16 * 1024 && (int64_t)p.group.d >= 4 * teams;
+    const int bytes = kRing + (p.in_smem ? (int)row : 0);
+    const int rc = allow_smem(reinterpret_cast<const void *>(layernorm_fwd_kernel<TX, TY, CH, NV>), kRing + 16 * 1024);
+    if (rc) return rc;
+    const int64_t ctas = (int64_t)sm_count() * (kRing > 64 * 1024 ? 2 : 3);
+    int64_t share = (p.rows + ctas - 1) / ctas;
+    share = (share + teams - 1) / teams * teams;
+    p.share = (uint32_t)share;
+    layernorm_fwd_kernel<TX, TY, CH, NV><<<(unsigned)((p.rows + share - 1) / share), kNormThreads, bytes, st>>>(p);
     return check_launch("layernorm_fwd_kernel launch");
 }
 
-// Chunks of a thread: up to 64 values (one row in a team's registers).  Few rows take the largest team
-// instead (256 threads): the row's loads are then in flight at once and the call is latency.
+// 128 bytes of a row per thread at most.
 template <typename TX, typename TY, int CH>
 static int pick_fwd(NormParams &p, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
-    const bool few = p.rows <= (uint32_t)(2 * sm_count());
-    p.team_log2 = team_of(chunks, few ? 1 : 64 / CH, 8);
+    p.team_log2 = team_of(chunks, 8, 8);
     const int64_t nv = (chunks + (1 << p.team_log2) - 1) >> p.team_log2;
     if (nv <= 1) return launch_fwd<TX, TY, CH, 1>(p, st);
     if (nv <= 2) return launch_fwd<TX, TY, CH, 2>(p, st);
     if (nv <= 4) return launch_fwd<TX, TY, CH, 4>(p, st);
     if (CH == 8 || nv <= 8) return launch_fwd<TX, TY, CH, 8>(p, st);
-    if (CH == 4 || nv <= 16) return launch_fwd<TX, TY, CH, CH == 8 ? 8 : 16>(p, st);
-    return launch_fwd<TX, TY, CH, CH == 1 ? 64 : 8>(p, st);
+    return launch_fwd<TX, TY, CH, CH == 8 ? 8 : 16>(p, st);
 }
 
 template <typename TX, typename TY>
-static int wide_or_narrow_fwd(NormParams &p, bool wide, cudaStream_t st) {
+static int any_fwd(NormParams &p, bool wide, cudaStream_t st) {
     constexpr int CH = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;     // 16 bytes of the wider type
-    return wide ? pick_fwd<TX, TY, CH>(p, st) : pick_fwd<TX, TY, 1>(p, st);
+    if (!wide) return pick_row<TX, TY, 1>(p, st);
+    // few rows: latency, not bandwidth
+    return p.rows <= (uint32_t)(2 * sm_count()) ? pick_row<TX, TY, CH>(p, st) : pick_fwd<TX, TY, CH>(p, st);
 }
 
 // Shares of the backward pass: the CTAs that the device holds at once, each with at least a round of rows.
@@ -445,29 +693,35 @@ static void bwd_shares(int64_t rows, int64_t cols, int64_t *share, int64_t *ctas
 
 template <typename TX, typename TY, int CH, int NV, int R, int T>
 static int launch_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
-    layernorm_bwd_kernel<TX, TY, CH, NV, R, T><<<(unsigned)ctas, T, 0, st>>>(p);
-    int rc = check_launch("layernorm_bwd_kernel launch");
+    constexpr int kBytes = BwdRing<TX, TY, CH, NV, R, T>::kBytes;
+    auto kernel = layernorm_bwd_kernel<TX, TY, CH, NV, R, T>;
+    int rc = allow_smem(reinterpret_cast<const void *>(kernel), kBytes);
+    if (rc) return rc;
+    kernel<<<(unsigned)ctas, T, kBytes, st>>>(p);
+    rc = check_launch("layernorm_bwd_kernel launch");
     if (rc || ctas == 1 || (!p.dw && !p.db)) return rc;
-    const dim3 grid((unsigned)((2 * (int64_t)p.cols + 31) / 32), (unsigned)(ctas - 1));
+    const int64_t groups = ((int64_t)p.rows + p.group.d - 1) / p.group.d;
+    p.by_group = groups < ctas;
+    const dim3 grid((unsigned)((2 * (int64_t)p.cols + 31) / 32), (unsigned)(p.by_group ? groups : ctas - 1));
     const cudaError_t e = launch_pdl(layernorm_grad_kernel, grid, dim3(32 * kGradRows), 0, st, p);
     return e == cudaSuccess ? NOMAS_OK : cuda_fail("layernorm_grad_kernel launch", (int)e, cudaGetErrorString(e));
 }
 
+// Values of a row per thread: 8 with 4 rows at a time, 16 with 2, then teams of 512 threads.
 template <typename TX, typename TY, int CH>
 static int pick_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
     p.team_log2 = team_of(chunks, 1, 8);
-    const int64_t values = ((chunks + 255) >> 8) * CH;
     if (chunks <= 256) return launch_bwd<TX, TY, CH, 1, 4, 256>(p, ctas, st);
-    if (values <= 8) return launch_bwd<TX, TY, CH, 8 / CH, 4, 256>(p, ctas, st);
-    if (values <= 16) return launch_bwd<TX, TY, CH, 16 / CH, 2, 256>(p, ctas, st);
+    if (p.cols <= 2048) return launch_bwd<TX, TY, CH, 8 / CH, CH == 1 ? 2 : 4, 256>(p, ctas, st);
+    if (p.cols <= 4096) return launch_bwd<TX, TY, CH, 16 / CH, CH == 1 ? 1 : 2, 256>(p, ctas, st);
     p.team_log2 = 9;
-    if (values <= 32) return launch_bwd<TX, TY, CH, 16 / CH, 1, 512>(p, ctas, st);
+    if (p.cols <= 8192) return launch_bwd<TX, TY, CH, 16 / CH, 1, 512>(p, ctas, st);
     return launch_bwd<TX, TY, CH, 32 / CH, 1, 512>(p, ctas, st);
 }
 
 template <typename TX, typename TY>
-static int wide_or_narrow_bwd(NormBwdParams &p, bool wide, int64_t ctas, cudaStream_t st) {
+static int any_bwd(NormBwdParams &p, bool wide, int64_t ctas, cudaStream_t st) {
     constexpr int CH = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;
     return wide ? pick_bwd<TX, TY, CH>(p, ctas, st) : pick_bwd<TX, TY, 1>(p, ctas, st);
 }
@@ -501,10 +755,10 @@ extern "C" int nomas_layernorm_fwd(const void *x, int64_t rows, int64_t cols, in
     if (dev.rc) return dev.rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (x_dtype == NOMAS_DTYPE_BF16)
-        return y_dtype == NOMAS_DTYPE_BF16 ? wide_or_narrow_fwd<__nv_bfloat16, __nv_bfloat16>(p, wide, st)
-                                           : wide_or_narrow_fwd<__nv_bfloat16, float>(p, wide, st);
-    return y_dtype == NOMAS_DTYPE_BF16 ? wide_or_narrow_fwd<float, __nv_bfloat16>(p, wide, st)
-                                       : wide_or_narrow_fwd<float, float>(p, wide, st);
+        return y_dtype == NOMAS_DTYPE_BF16 ? any_fwd<__nv_bfloat16, __nv_bfloat16>(p, wide, st)
+                                           : any_fwd<__nv_bfloat16, float>(p, wide, st);
+    return y_dtype == NOMAS_DTYPE_BF16 ? any_fwd<float, __nv_bfloat16>(p, wide, st)
+                                       : any_fwd<float, float>(p, wide, st);
 }
 
 extern "C" size_t nomas_layernorm_workspace_bytes(int64_t rows, int64_t cols, int64_t rows_per_group) {
@@ -552,10 +806,11 @@ extern "C" int nomas_layernorm_bwd(const void *dy, int64_t lddy, int y_dtype, co
     p.group = group_div(rows, rows_per_group);
     p.p_bf16 = p_dtype == NOMAS_DTYPE_BF16;
     p.unit = unit_offset && w ? 1.0f : 0.0f;
+    p.grad_wide = wide_ok(dw, ldg) && wide_ok(db, ldg);
     const bool wide = cols % 8 == 0 && wide_ok(dy, lddy) && wide_ok(x, ldx) && wide_ok(w, ldp) && wide_ok(dx, lddx);
     if (x_dtype == NOMAS_DTYPE_BF16)
-        return y_dtype == NOMAS_DTYPE_BF16 ? wide_or_narrow_bwd<__nv_bfloat16, __nv_bfloat16>(p, wide, ctas, st)
-                                           : wide_or_narrow_bwd<__nv_bfloat16, float>(p, wide, ctas, st);
-    return y_dtype == NOMAS_DTYPE_BF16 ? wide_or_narrow_bwd<float, __nv_bfloat16>(p, wide, ctas, st)
-                                       : wide_or_narrow_bwd<float, float>(p, wide, ctas, st);
+        return y_dtype == NOMAS_DTYPE_BF16 ? any_bwd<__nv_bfloat16, __nv_bfloat16>(p, wide, ctas, st)
+                                           : any_bwd<__nv_bfloat16, float>(p, wide, ctas, st);
+    return y_dtype == NOMAS_DTYPE_BF16 ? any_bwd<float, __nv_bfloat16>(p, wide, ctas, st)
+                                       : any_bwd<float, float>(p, wide, ctas, st);
 }
