@@ -9,13 +9,14 @@
 //                          and layouts that allow no wide loads
 //   layernorm_fwd_kernel   forward, a CTA takes a contiguous share of the rows.  Every thread keeps its own
 //                          ring of 16-byte chunks in shared memory, filled by asynchronous copies several rows
-//                          ahead (nothing to synchronise: a thread reads what it copied), and the group's
-//                          weight and bias rows wait in shared memory too.
-//   layernorm_bwd_kernel   a CTA takes a contiguous share of the rows, R rows of each team at a time, through
-//                          the same rings; a thread owns columns, so dw and db of a group add up in its
-//                          registers in row order.  Groups inside a share are written at once; where a group
+//                          ahead (nothing to synchronise: a thread reads what it copied).  A thread owns
+//                          columns, whose weight and bias stay in its registers for a group, and takes R rows
+//                          at a time, which share the two exchanges of sums between the warps.
+//   layernorm_bwd_kernel   the same for dy and x; dw and db of a group add up in the registers in row order.  Groups inside a share are written at once; where a group
 //                          goes on in the next share, its sums so far go to the workspace (two slots a CTA).
 //   layernorm_grad_kernel  adds up the shares of such groups, in share order.
+#include <atomic>
+
 #include "common.cuh"
 
 namespace nomas {
@@ -33,7 +34,6 @@ struct NormParams {
     int32_t p_bf16;
     float unit, eps;
     uint32_t share;             // rows of a CTA (layernorm_fwd_kernel)
-    int32_t in_smem;            // it keeps the group's parameters in shared memory
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -100,6 +100,53 @@ __device__ __forceinline__ void load_param(const void *base, int32_t bf16, int64
         load_chunk<CH>(static_cast<const float *>(base) + at, v);
 }
 
+// Two fp32 values in a register pair: the packed instructions of sm_100 do two roundings of fp32 each, at half the
+// issue slots.  The wide kernels are close to bound by issue otherwise (forward, 26400 x 2048: 22 instructions a
+// value and 56 us with scalar sums).
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void pair_split(Pair v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ float pair_sum(Pair v) {
+    float lo, hi;
+    pair_split(v, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// CH consecutive values (4 or 8) at p as pairs, and back.
+template <int CH, typename T>
+__device__ __forceinline__ void load_pairs(const T *p, Pair (&v)[CH / 2]) {
+    float f[CH];
+    load_chunk<CH>(p, f);
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) v[i] = pair_of(f[2 * i], f[2 * i + 1]);
+}
+template <int CH, typename T>
+__device__ __forceinline__ void store_pairs(T *p, const Pair (&v)[CH / 2]) {
+    float f[CH];
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) pair_split(v[i], f[2 * i], f[2 * i + 1]);
+    store_chunk<CH>(p, f);
+}
+
 // Sums of N values (N = 1, 2, 4, 8) over a team of 2^log2 threads; every thread gets them, in an order that
 // depends on the team alone.  In a warp the N values are halved between the lanes as they are added up (N - 1
 // + log2(32 / N) shuffles, not 5 N).  Teams of more than a warp meet in `red` (N floats per warp of the CTA and
@@ -146,13 +193,15 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int log2, float *red, in
     for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, s, i * step);
 }
 
-// Asynchronous copy of a chunk of BYTES (8 or 16) into shared memory, in the groups that ring_commit closes.
+// Asynchronous copy of a chunk of BYTES (8 or 16) into shared memory, in the groups that ring_commit closes; zeros
+// and no read where it is not live, so that the reader needs no branch.
 template <int BYTES>
-__device__ __forceinline__ void ring_load(uint32_t dst, const void *src) {
+__device__ __forceinline__ void ring_load(uint32_t dst, const void *src, bool live) {
+    const int n = live ? BYTES : 0;
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
 }
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest N groups of this thread have landed.
@@ -184,7 +233,7 @@ __device__ __forceinline__ float centre_row(float (&v)[NV][CH], int lane, const 
         }
     }
     team_sum<1>(s, p.team_log2, red, parity);
-    return 1.0f / sqrtf(s[0] / (float)p.cols + p.eps);
+    return rsqrtf(s[0] / (float)p.cols + p.eps);
 }
 
 template <typename TX, typename TY, int CH, int NV>
@@ -225,42 +274,47 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_row_kernel(const NormP
     }
 }
 
-// Stages of the forward ring: about 256 bytes a thread in flight.
-template <int NV>
+// Forward ring: stages of R rows of x, two to four, so that three CTAs of 256 threads (one of 512) fit an SM.
+template <typename TX, int CH, int NV, int R, int T>
 struct FwdRing {
-    static constexpr int kStages = NV >= 8 ? 3 : NV == 4 ? 5 : 8;
+    static constexpr int kStage = R * NV * CH * (int)sizeof(TX) * T;
+    static constexpr int kFit = (T == 256 ? 72 : 200) * 1024 / kStage;
+    static constexpr int kStages = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
+    static constexpr int kBytes = kStages * kStage;
 };
 
-template <typename TX, typename TY, int CH, int NV>
-__global__ void __launch_bounds__(kNormThreads, NV * CH > 32 ? 2 : 3) layernorm_fwd_kernel(const NormParams p) {
-    constexpr int S = FwdRing<NV>::kStages, BYTES = CH * sizeof(TX);
+template <typename TX, typename TY, int CH, int NV, int R, int T>
+__global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(const NormParams p) {
+    constexpr int S = FwdRing<TX, CH, NV, R, T>::kStages, BYTES = CH * sizeof(TX), P = CH / 2;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float red[2 * kNormThreads / 32];
+    __shared__ float red[2 * (T / 32) * R];
     const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), mine = threadIdx.x >> p.team_log2;
-    const uint32_t teams = kNormThreads >> p.team_log2;
+    const uint32_t teams = T >> p.team_log2;
     const uint32_t begin = blockIdx.x * p.share, end = min(p.rows, begin + p.share);
-    const uint32_t ring = smem_u32(smem) + threadIdx.x * BYTES;
-    const uint8_t *ring_at = smem + threadIdx.x * BYTES;
-    uint8_t *params = smem + S * NV * kNormThreads * BYTES;
-    const int64_t psize = p.p_bf16 ? 2 : 4;
+    const uint8_t *ring = smem + threadIdx.x * BYTES;
+    const float inv = 1.0f / (float)p.cols;
     int parity = 0;
-    // the rounds of the share in order: `teams` rows from fetch_row, inside a run of rows that share parameters
-    // (the whole share when they are read from global memory: groups of few rows, or rows too wide)
+    // the batches of the share in order: R * teams rows from fetch_row, inside the group that ends at fetch_stop
     uint32_t fetch_row = begin, fetch_stop = begin;
-    auto run_end = [&](uint32_t row) {
-        return p.in_smem ? (uint32_t)min((int64_t)end, ((int64_t)fdiv(row, p.group) + 1) * p.group.d) : end;
-    };
+    const uint32_t ring_at = smem_u32(ring);
+    const TX *from = static_cast<const TX *>(p.x) + (int64_t)mine * p.ldx + lane * CH;
+    const int64_t row_step = (int64_t)teams * p.ldx;
     auto fetch = [&](int stage) {
         if (fetch_row < end) {
-            if (fetch_row >= fetch_stop) fetch_stop = run_end(fetch_row);
-            const uint32_t at = fetch_row + mine;
-            const TX *x = static_cast<const TX *>(p.x) + (int64_t)at * p.ldx;
+            if (fetch_row >= fetch_stop)
+                fetch_stop = (uint32_t)min((int64_t)end, ((int64_t)fdiv(fetch_row, p.group) + 1) * p.group.d);
+            const TX *x = from + fetch_row * p.ldx;
+            const uint32_t to = ring_at + stage * (R * NV * T * BYTES);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const uint32_t c = (uint32_t)(lane + j * team) * CH;
-                if (at < fetch_stop && c < p.cols) ring_load<BYTES>(ring + (stage * NV + j) * kNormThreads * BYTES, x + c);
+            for (int r = 0; r < R; ++r, x += row_step) {
+                const bool live = fetch_row + r * teams + mine < fetch_stop;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const bool in = live && (uint32_t)(lane + j * team) * CH < p.cols;
+                    ring_load<BYTES>(to + (r * NV + j) * T * BYTES, in ? x + j * team * CH : p.x, in);
+                }
             }
-            fetch_row = min(fetch_row + teams, fetch_stop);
+            fetch_row = min(fetch_row + R * teams, fetch_stop);
         }
         ring_commit();
     };
@@ -268,53 +322,77 @@ __global__ void __launch_bounds__(kNormThreads, NV * CH > 32 ? 2 : 3) layernorm_
     for (int k = 0; k < S - 1; ++k) fetch(k);
     int stage = 0, last = S - 1;
     for (uint32_t row = begin; row < end;) {
-        const uint32_t stop = run_end(row);
-        if (p.in_smem) {
-            const int64_t from = (int64_t)fdiv(row, p.group) * p.ldp * psize, bytes = (int64_t)p.cols * psize;
-            __syncthreads();
-            for (int64_t o = threadIdx.x * 16; o < bytes; o += kNormThreads * 16) {
-                if (p.w) *reinterpret_cast<uint4 *>(params + o) = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.w) + from + o);
-                if (p.b) *reinterpret_cast<uint4 *>(params + bytes + o) = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.b) + from + o);
+        const uint32_t g = fdiv(row, p.group), stop = (uint32_t)min((int64_t)end, ((int64_t)g + 1) * p.group.d);
+        Pair f[NV][P], b[NV][P];                // u + w and b of this thread's columns
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t c = (uint32_t)(lane + j * team) * CH;
+            float w[CH], bias[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) w[i] = 1.0f - p.unit, bias[i] = 0.0f;
+            if (p.w && c < p.cols) load_param<CH>(p.w, p.p_bf16, (int64_t)g * p.ldp + c, w);
+            if (p.b && c < p.cols) load_param<CH>(p.b, p.p_bf16, (int64_t)g * p.ldp + c, bias);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                f[j][i] = pair_of(p.unit + w[2 * i], p.unit + w[2 * i + 1]);
+                b[j][i] = pair_of(bias[2 * i], bias[2 * i + 1]);
             }
-            __syncthreads();
         }
-        for (uint32_t r0 = row; r0 < stop; r0 += teams) {
-            const uint32_t at = r0 + mine;
-            const bool live = at < stop;        // every thread takes part in the sums
+        for (uint32_t r0 = row; r0 < stop; r0 += teams * R) {
             fetch(last);
             ring_wait<S - 1>();
-            float v[NV][CH];
+            Pair v[R][NV][P];
+            float s[R], mean[R];
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const uint32_t c = (uint32_t)(lane + j * team) * CH;
+            for (int r = 0; r < R; ++r) {
+                Pair sum = 0;
 #pragma unroll
-                for (int i = 0; i < CH; ++i) v[j][i] = 0.0f;
-                if (live && c < p.cols) load_chunk<CH>(reinterpret_cast<const TX *>(ring_at + (stage * NV + j) * kNormThreads * BYTES), v[j]);
+                for (int j = 0; j < NV; ++j) {
+                    load_pairs<CH>(reinterpret_cast<const TX *>(ring + ((stage * R + r) * NV + j) * T * BYTES), v[r][j]);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) sum = add2(sum, v[r][j][i]);
+                }
+                s[r] = pair_sum(sum);
             }
             last = stage;
             stage = stage + 1 == S ? 0 : stage + 1;
-            float mean;
-            const float rstd = centre_row<CH, NV>(v, lane, p, red, parity, mean);
-            if (!live) continue;
-            if (lane == 0) {
-                if (p.mean) p.mean[at] = mean;
-                if (p.rstd) p.rstd[at] = rstd;
+            team_sum<R>(s, p.team_log2, red, parity);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                mean[r] = s[r] * inv;
+                const Pair minus = pair_of(-mean[r], -mean[r]);
+                Pair sum = 0;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const Pair before = sum;
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        v[r][j][i] = add2(v[r][j][i], minus);
+                        sum = fma2(v[r][j][i], v[r][j][i], sum);
+                    }
+                    if ((uint32_t)(lane + j * team) * CH >= p.cols) sum = before;       // no column
+                }
+                s[r] = pair_sum(sum);
             }
-            const void *wr = p.in_smem ? params : p.w, *br = p.in_smem ? params + p.cols * psize : p.b;
-            const int64_t pg = p.in_smem ? 0 : (int64_t)fdiv(at, p.group) * p.ldp;
-            TY *y = static_cast<TY *>(p.y) + (int64_t)at * p.ldy;
+            team_sum<R>(s, p.team_log2, red, parity);
+            TY *y = static_cast<TY *>(p.y) + (int64_t)(r0 + mine) * p.ldy + lane * CH;
+            const int64_t out_step = (int64_t)teams * p.ldy;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const uint32_t c = (uint32_t)(lane + j * team) * CH;
-                if (c >= p.cols) continue;
-                float w[CH], b[CH];
+            for (int r = 0; r < R; ++r, y += out_step) {
+                const uint32_t at = r0 + r * teams + mine;
+                const float rstd = rsqrtf(s[r] * inv + p.eps);
+                if (at >= stop) continue;
+                if (lane == 0) {
+                    if (p.mean) p.mean[at] = mean[r];
+                    if (p.rstd) p.rstd[at] = rstd;
+                }
+                const Pair scale = pair_of(rstd, rstd);
 #pragma unroll
-                for (int i = 0; i < CH; ++i) w[i] = 1.0f - p.unit, b[i] = 0.0f;
-                if (p.w) load_param<CH>(wr, p.p_bf16, pg + c, w);
-                if (p.b) load_param<CH>(br, p.p_bf16, pg + c, b);
+                for (int j = 0; j < NV; ++j) {
 #pragma unroll
-                for (int i = 0; i < CH; ++i) v[j][i] = fmaf(v[j][i] * rstd, p.unit + w[i], b[i]);
-                store_chunk<CH>(y + c, v[j]);
+                    for (int i = 0; i < P; ++i) v[r][j][i] = fma2(mul2(v[r][j][i], scale), f[j][i], b[j][i]);
+                    if ((uint32_t)(lane + j * team) * CH < p.cols) store_pairs<CH>(y + j * team * CH, v[r][j]);
+                }
             }
         }
         row = stop;
@@ -335,25 +413,37 @@ struct NormBwdParams {
     float unit;
 };
 
+// Whether several teams of a CTA can share columns: a thread with more values has a team as large as the CTA.
+template <int CH, int NV>
+constexpr bool MEET = NV == 1 || (CH == 1 && NV == 2);
+
 // dw and db of a group (or of a part of one) from the CTA's threads: teams of the CTA hold the same columns.
 template <int CH, int NV, int T>
-__device__ __forceinline__ void flush_grads(const NormBwdParams &p, float (&aw)[NV][CH], float (&ab)[NV][CH], float *dw,
-                                            float *db, bool wide, float *meet) {
+__device__ __forceinline__ void flush_grads(const NormBwdParams &p, Pair (&sum_w)[NV * CH / 2], Pair (&sum_b)[NV * CH / 2],
+                                            float *dw, float *db, bool wide, float *meet) {
+    float aw[NV][CH], ab[NV][CH];
+#pragma unroll
+    for (int k = 0; k < NV * CH / 2; ++k) {
+        pair_split(sum_w[k], aw[2 * k / CH][2 * k % CH], aw[(2 * k + 1) / CH][(2 * k + 1) % CH]);
+        pair_split(sum_b[k], ab[2 * k / CH][2 * k % CH], ab[(2 * k + 1) / CH][(2 * k + 1) % CH]);
+        sum_w[k] = sum_b[k] = 0;
+    }
     const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), teams = T >> p.team_log2;
-    if (NV == 1 && teams > 1) { // a larger NV has one team
-        const int stride = team * CH, mine = threadIdx.x >> p.team_log2;
+    if (MEET<CH, NV> && teams > 1) {
+        const int stride = team * CH * NV, mine = threadIdx.x >> p.team_log2;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < CH; ++i) meet[mine * stride + i * team + lane] = g ? ab[0][i] : aw[0][i];
+            for (int i = 0; i < CH * NV; ++i)
+                meet[mine * stride + i * team + lane] = g ? ab[i / CH][i % CH] : aw[i / CH][i % CH];
             __syncthreads();
             if (mine == 0) {
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
+                for (int i = 0; i < CH * NV; ++i) {
                     float s = 0.0f;
                     for (int k = 0; k < teams; ++k) s += meet[k * stride + i * team + lane];
-                    (g ? ab[0][i] : aw[0][i]) = s;
+                    (g ? ab[i / CH][i % CH] : aw[i / CH][i % CH]) = s;
                 }
             }
         }
@@ -375,10 +465,6 @@ __device__ __forceinline__ void flush_grads(const NormBwdParams &p, float (&aw)[
             }
         }
     }
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < CH; ++i) aw[j][i] = ab[j][i] = 0.0f;
 }
 
 // Backward ring: stages of R rows of x and dy, up to three in about 200 KB; without two (rows above 8192 columns
@@ -397,38 +483,39 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwd
     constexpr int S = RING ? BwdRing<TX, TY, CH, NV, R, T>::kStages : 1, XB = CH * sizeof(TX), YB = CH * sizeof(TY);
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2 * (T / 32) * 2 * R];
-    __shared__ float meet[NV == 1 ? T * CH : 1];
+    __shared__ float meet[MEET<CH, NV> ? T * CH * NV : 1];
     const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), mine = threadIdx.x >> p.team_log2;
     const uint32_t teams = T >> p.team_log2;
     const uint32_t begin = blockIdx.x * p.share, end = min(p.rows, begin + p.share);
-    float aw[NV][CH], ab[NV][CH];
+    constexpr int E = NV * CH, P = E / 2;       // values of a row per thread, in pairs
+    Pair aw[P], ab[P];
     int parity = 0;
     const float inv = 1.0f / (float)p.cols;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < CH; ++i) aw[j][i] = ab[j][i] = 0.0f;
+    for (int k = 0; k < P; ++k) aw[k] = ab[k] = 0;
 
     // the batches of the share in order: R * teams rows from fetch_row, inside the group that ends at fetch_stop
     uint32_t fetch_row = begin, fetch_stop = begin;
     const uint8_t *ring_x = smem + threadIdx.x * XB, *ring_y = smem + S * R * NV * T * XB + threadIdx.x * YB;
+    const uint32_t at_x = smem_u32(ring_x), at_y = smem_u32(ring_y);
+    const TX *from_x = static_cast<const TX *>(p.x) + (int64_t)mine * p.ldx + lane * CH;
+    const TY *from_y = static_cast<const TY *>(p.dy) + (int64_t)mine * p.lddy + lane * CH;
+    const int64_t step_x = (int64_t)teams * p.ldx, step_y = (int64_t)teams * p.lddy;
     auto fetch = [&](int stage) {
         if (fetch_row < end) {
             if (fetch_row >= fetch_stop)
                 fetch_stop = (uint32_t)min((int64_t)end, ((int64_t)fdiv(fetch_row, p.group) + 1) * p.group.d);
+            const TX *x = from_x + fetch_row * p.ldx;
+            const TY *dy = from_y + fetch_row * p.lddy;
+            const uint32_t to_x = at_x + stage * (R * NV * T * XB), to_y = at_y + stage * (R * NV * T * YB);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t at = fetch_row + r * teams + mine;
-                if (at >= fetch_stop) continue;
-                const TX *x = static_cast<const TX *>(p.x) + (int64_t)at * p.ldx;
-                const TY *dy = static_cast<const TY *>(p.dy) + (int64_t)at * p.lddy;
+            for (int r = 0; r < R; ++r, x += step_x, dy += step_y) {
+                const bool live = fetch_row + r * teams + mine < fetch_stop;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const uint32_t c = (uint32_t)(lane + j * team) * CH;
-                    if (c >= p.cols) continue;
-                    const int slot = (stage * R + r) * NV + j;
-                    ring_load<RING ? XB : 16>(smem_u32(ring_x + slot * T * XB), x + c);
-                    ring_load<RING ? YB : 16>(smem_u32(ring_y + slot * T * YB), dy + c);
+                    const bool in = live && (uint32_t)(lane + j * team) * CH < p.cols;
+                    ring_load<RING ? XB : 16>(to_x + (r * NV + j) * T * XB, in ? x + j * team * CH : p.x, in);
+                    ring_load<RING ? YB : 16>(to_y + (r * NV + j) * T * YB, in ? dy + j * team * CH : p.dy, in);
                 }
             }
             fetch_row = min(fetch_row + R * teams, fetch_stop);
@@ -444,18 +531,23 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwd
         const uint32_t g = fdiv(row, p.group);
         const int64_t g0 = (int64_t)g * p.group.d, g1 = min(g0 + (int64_t)p.group.d, (int64_t)p.rows);
         const uint32_t stop = (uint32_t)min((int64_t)end, g1);
-        float f[NV][CH];                        // u + w
+        Pair f[P];                              // u + w
+        {
+            float w[NV][CH];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const uint32_t c = (uint32_t)(lane + j * team) * CH;
+            for (int j = 0; j < NV; ++j) {
+                const uint32_t c = (uint32_t)(lane + j * team) * CH;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) f[j][i] = 1.0f - p.unit;
-            if (p.w && c < p.cols) load_param<CH>(p.w, p.p_bf16, (int64_t)g * p.ldp + c, f[j]);
+                for (int i = 0; i < CH; ++i) w[j][i] = 1.0f - p.unit;
+                if (p.w && c < p.cols) load_param<CH>(p.w, p.p_bf16, (int64_t)g * p.ldp + c, w[j]);
+            }
 #pragma unroll
-            for (int i = 0; i < CH; ++i) f[j][i] += p.unit;
+            for (int k = 0; k < P; ++k)
+                f[k] = pair_of(p.unit + w[2 * k / CH][2 * k % CH], p.unit + w[(2 * k + 1) / CH][(2 * k + 1) % CH]);
         }
         for (uint32_t r0 = row; r0 < stop; r0 += teams * R) {
-            float mean[R], rstd[R], xh[R][NV][CH], gy[R][NV][CH], s[2 * R];
+            float mean[R], rstd[R], s[2 * R];
+            Pair xh[R][P], gy[R][P];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const uint32_t at = r0 + r * teams + mine;
@@ -472,59 +564,64 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwd
                 const bool live = at < stop;
                 const TX *x = static_cast<const TX *>(p.x) + (int64_t)at * p.ldx;
                 const TY *dy = static_cast<const TY *>(p.dy) + (int64_t)at * p.lddy;
+                float fx[NV][CH], fy[NV][CH];
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const uint32_t c = (uint32_t)(lane + j * team) * CH;
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) xh[r][j][i] = gy[r][j][i] = 0.0f;
-                    if (!live || c >= p.cols) continue;
+                    for (int i = 0; i < CH; ++i) fx[j][i] = fy[j][i] = 0.0f;
                     if constexpr (RING) {
                         const int slot = (stage * R + r) * NV + j;
-                        load_chunk<CH>(reinterpret_cast<const TX *>(ring_x + slot * T * XB), xh[r][j]);
-                        load_chunk<CH>(reinterpret_cast<const TY *>(ring_y + slot * T * YB), gy[r][j]);
-                    } else {
-                        load_chunk<CH>(x + c, xh[r][j]);
-                        load_chunk<CH>(dy + c, gy[r][j]);
+                        load_chunk<CH>(reinterpret_cast<const TX *>(ring_x + slot * T * XB), fx[j]);
+                        load_chunk<CH>(reinterpret_cast<const TY *>(ring_y + slot * T * YB), fy[j]);
+                    } else if (live && c < p.cols) {
+                        load_chunk<CH>(x + c, fx[j]);
+                        load_chunk<CH>(dy + c, fy[j]);
                     }
+                }
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    xh[r][k] = pair_of(fx[2 * k / CH][2 * k % CH], fx[(2 * k + 1) / CH][(2 * k + 1) % CH]);
+                    gy[r][k] = pair_of(fy[2 * k / CH][2 * k % CH], fy[(2 * k + 1) / CH][(2 * k + 1) % CH]);
                 }
             }
             last = stage;
             stage = stage + 1 == S ? 0 : stage + 1;
+            // columns past the row and rows past the group have dy = 0: what their xhat is adds nothing
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                s[2 * r] = s[2 * r + 1] = 0.0f;
+                const Pair minus = pair_of(-mean[r], -mean[r]), scale = pair_of(rstd[r], rstd[r]);
+                Pair s1 = 0, s2 = 0;
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const bool in = (uint32_t)(lane + j * team) * CH < p.cols;
-#pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        const float xv = in ? (xh[r][j][i] - mean[r]) * rstd[r] : 0.0f, d = gy[r][j][i];
-                        aw[j][i] = fmaf(d, xv, aw[j][i]);
-                        ab[j][i] += d;
-                        const float gv = d * f[j][i];
-                        s[2 * r] += gv;
-                        s[2 * r + 1] = fmaf(gv, xv, s[2 * r + 1]);
-                        xh[r][j][i] = xv;
-                        gy[r][j][i] = gv;
-                    }
+                for (int k = 0; k < P; ++k) {
+                    const Pair xv = mul2(add2(xh[r][k], minus), scale), d = gy[r][k], gv = mul2(d, f[k]);
+                    aw[k] = fma2(d, xv, aw[k]);
+                    ab[k] = add2(ab[k], d);
+                    s1 = add2(s1, gv);
+                    s2 = fma2(gv, xv, s2);
+                    xh[r][k] = xv;
+                    gy[r][k] = gv;
                 }
+                s[2 * r] = pair_sum(s1);
+                s[2 * r + 1] = pair_sum(s2);
             }
             if (!p.dx) continue;
             team_sum<2 * R>(s, p.team_log2, red, parity);
+            TX *dx = static_cast<TX *>(p.dx) + (int64_t)(r0 + mine) * p.lddx + lane * CH;
+            const int64_t out_step = (int64_t)teams * p.lddx;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t at = r0 + r * teams + mine;
-                if (at >= stop) continue;
-                TX *dx = static_cast<TX *>(p.dx) + (int64_t)at * p.lddx;
+            for (int r = 0; r < R; ++r, dx += out_step) {
+                if (r0 + r * teams + mine >= stop) continue;
                 const float m1 = s[2 * r] * inv, m2 = s[2 * r + 1] * inv;
+                const Pair minus1 = pair_of(-m1, -m1), minus2 = pair_of(-m2, -m2), scale = pair_of(rstd[r], rstd[r]);
+                float out[NV][CH];
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const uint32_t c = (uint32_t)(lane + j * team) * CH;
-                    if (c >= p.cols) continue;
+                for (int k = 0; k < P; ++k)
+                    pair_split(mul2(scale, fma2(xh[r][k], minus2, add2(gy[r][k], minus1))), out[2 * k / CH][2 * k % CH],
+                               out[(2 * k + 1) / CH][(2 * k + 1) % CH]);
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) gy[r][j][i] = rstd[r] * (gy[r][j][i] - m1 - xh[r][j][i] * m2);
-                    store_chunk<CH>(dx + c, gy[r][j]);
-                }
+                for (int j = 0; j < NV; ++j)
+                    if ((uint32_t)(lane + j * team) * CH < p.cols) store_chunk<CH>(dx + j * team * CH, out[j]);
             }
         }
         if (p.dw || p.db) {
@@ -615,12 +712,22 @@ static int team_of(int64_t chunks, int per, int most) {
     return l > most ? most : l;
 }
 
-// Dynamic shared memory above 48 KB has to be allowed per kernel and device.
-static int allow_smem(const void *kernel, int bytes) {
-    if (bytes <= 48 * 1024) return NOMAS_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    return e == cudaSuccess ? NOMAS_OK : cuda_fail("cudaFuncSetAttribute(layer norm smem)", (int)e, cudaGetErrorString(e));
-}
+// Dynamic shared memory above 48 KB has to be allowed per kernel and device: once for the largest size asked for.
+struct SmemAllowed {
+    std::atomic<int> bytes[64] = {};
+    int operator()(const void *kernel, int want) {
+        if (want <= 48 * 1024) return NOMAS_OK;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && dev >= 0 && dev < 64 && bytes[dev].load() >= want) return NOMAS_OK;
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, want);
+        if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(layer norm smem)", (int)e, cudaGetErrorString(e));
+        int had = dev < 64 ? bytes[dev].load() : want;
+        while (had < want && !bytes[dev].compare_exchange_weak(had, want)) {
+        }
+        return NOMAS_OK;
+    }
+};
 
 template <typename TX, typename TY, int CH, int NV>
 static int launch_row(const NormParams &p, cudaStream_t st) {
@@ -643,35 +750,32 @@ static int pick_row(NormParams &p, cudaStream_t st) {
     return launch_row<TX, TY, CH, CH == 1 ? 64 : 8>(p, st);
 }
 
-template <typename TX, typename TY, int CH, int NV>
+template <typename TX, typename TY, int CH, int NV, int R, int T>
 static int launch_fwd(NormParams &p, cudaStream_t st) {
-    constexpr int kRing = FwdRing<NV>::kStages * NV * CH * (int)sizeof(TX) * kNormThreads;
-    const int64_t row = 2 * (int64_t)p.cols * (p.p_bf16 ? 2 : 4);
-    // a group's parameters are loaded once a CTA: worth it from a few rounds of rows on
-    const int64_t teams = kNormThreads >> p.team_log2;
-    p.in_smem = (p.w || p.b) && row <= 16 * 1024 && (int64_t)p.group.d >= 4 * teams;
-    const int bytes = kRing + (p.in_smem ? (int)row : 0);
-    const int rc = allow_smem(reinterpret_cast<const void *>(layernorm_fwd_kernel<TX, TY, CH, NV>), kRing + 16 * 1024);
+    constexpr int kBytes = FwdRing<TX, CH, NV, R, T>::kBytes;
+    auto kernel = layernorm_fwd_kernel<TX, TY, CH, NV, R, T>;
+    static SmemAllowed allowed;
+    const int rc = allowed(reinterpret_cast<const void *>(kernel), kBytes);
     if (rc) return rc;
-    const int64_t ctas = (int64_t)sm_count() * (kRing > 64 * 1024 ? 2 : 3);
+    const int64_t teams = T >> p.team_log2, ctas = (int64_t)sm_count() * (T == 512 ? 1 : kBytes > 74 * 1024 ? 2 : 3);
     int64_t share = (p.rows + ctas - 1) / ctas;
-    share = (share + teams - 1) / teams * teams;
+    if (share < teams) share = teams;
     p.share = (uint32_t)share;
-    layernorm_fwd_kernel<TX, TY, CH, NV><<<(unsigned)((p.rows + share - 1) / share), kNormThreads, bytes, st>>>(p);
+    kernel<<<(unsigned)((p.rows + share - 1) / share), T, kBytes, st>>>(p);
     return check_launch("layernorm_fwd_kernel launch");
 }
 
-// 128 bytes of a row per thread at most.
+// Values of a row per thread: 8 with 4 rows at a time, 16 with 2, then teams of 512 threads.
 template <typename TX, typename TY, int CH>
 static int pick_fwd(NormParams &p, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
-    p.team_log2 = team_of(chunks, 8, 8);
-    const int64_t nv = (chunks + (1 << p.team_log2) - 1) >> p.team_log2;
-    if (nv <= 1) return launch_fwd<TX, TY, CH, 1>(p, st);
-    if (nv <= 2) return launch_fwd<TX, TY, CH, 2>(p, st);
-    if (nv <= 4) return launch_fwd<TX, TY, CH, 4>(p, st);
-    if (CH == 8 || nv <= 8) return launch_fwd<TX, TY, CH, 8>(p, st);
-    return launch_fwd<TX, TY, CH, CH == 8 ? 8 : 16>(p, st);
+    p.team_log2 = team_of(chunks, 1, 8);
+    if (chunks <= 256) return launch_fwd<TX, TY, CH, 1, 4, 256>(p, st);
+    if (p.cols <= 2048) return launch_fwd<TX, TY, CH, 8 / CH, 4, 256>(p, st);
+    if (p.cols <= 4096) return launch_fwd<TX, TY, CH, 16 / CH, 2, 256>(p, st);
+    p.team_log2 = 9;
+    if (p.cols <= 8192) return launch_fwd<TX, TY, CH, 16 / CH, 2, 512>(p, st);
+    return launch_fwd<TX, TY, CH, 32 / CH, 1, 512>(p, st);
 }
 
 template <typename TX, typename TY>
@@ -695,7 +799,8 @@ template <typename TX, typename TY, int CH, int NV, int R, int T>
 static int launch_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     constexpr int kBytes = BwdRing<TX, TY, CH, NV, R, T>::kBytes;
     auto kernel = layernorm_bwd_kernel<TX, TY, CH, NV, R, T>;
-    int rc = allow_smem(reinterpret_cast<const void *>(kernel), kBytes);
+    static SmemAllowed allowed;
+    int rc = allowed(reinterpret_cast<const void *>(kernel), kBytes);
     if (rc) return rc;
     kernel<<<(unsigned)ctas, T, kBytes, st>>>(p);
     rc = check_launch("layernorm_bwd_kernel launch");
@@ -711,8 +816,9 @@ static int launch_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
 template <typename TX, typename TY, int CH>
 static int pick_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
-    p.team_log2 = team_of(chunks, 1, 8);
-    if (chunks <= 256) return launch_bwd<TX, TY, CH, 1, 4, 256>(p, ctas, st);
+    constexpr int kLeast = CH == 1 ? 2 : 1;     // pairs of values
+    p.team_log2 = team_of(chunks, kLeast, 8);
+    if (chunks <= kLeast * 256) return launch_bwd<TX, TY, CH, kLeast, 4, 256>(p, ctas, st);
     if (p.cols <= 2048) return launch_bwd<TX, TY, CH, 8 / CH, CH == 1 ? 2 : 4, 256>(p, ctas, st);
     if (p.cols <= 4096) return launch_bwd<TX, TY, CH, 16 / CH, CH == 1 ? 1 : 2, 256>(p, ctas, st);
     p.team_log2 = 9;
