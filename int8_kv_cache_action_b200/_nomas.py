@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnomas.so")
 if not os.path.exists(_LIB_PATH):
@@ -29,6 +30,7 @@ NOMAS_ROPE_INTERLEAVED, NOMAS_ROPE_HALVES = 0, 1
 NOMAS_ROPE_MAX_TENSORS = 4
 NOMAS_ROPE_MAX_HEAD_DIM = 256
 NOMAS_NORM_MAX_COLS = 16384
+NOMAS_W4_FEW_ROWS = 64
 
 EXPORTED = ["nomas_kv_cache_bytes", "nomas_kv_cache_init", "nomas_kv_cache_destroy", "nomas_kv_cache_state",
             "nomas_kv_append", "nomas_mask_layout_query", "nomas_mask_bytes", "nomas_mask_build",
@@ -130,8 +132,8 @@ _sigs = {
     "nomas_w8a16_linear": (ctypes.c_int, [_p, _i64, _i64, _i64, _p, _p, _i64, _p, _i64, ctypes.c_int, _p, _p,
                                           _p]),
     "nomas_status_read": (ctypes.c_int, [_p, _p]),
-    "nomas_rope": (ctypes.c_int, [ctypes.POINTER(nomas_rope_spec), ctypes.POINTER(nomas_rope_grid), _p, _i64,
-                                  ctypes.POINTER(nomas_rope_tensor), ctypes.c_int, ctypes.c_int, ctypes.c_int, _p]),
+    # structures by address: byref, an array, or packed bytes
+    "nomas_rope": (ctypes.c_int, [_p, _p, _p, _i64, _p, ctypes.c_int, ctypes.c_int, ctypes.c_int, _p]),
     "nomas_layernorm_fwd": (ctypes.c_int, [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p, _i64, ctypes.c_int, _i64,
                                            ctypes.c_int, _f32, _p, _i64, ctypes.c_int, _p, _p, _p]),
     "nomas_layernorm_workspace_bytes": (_sz, [_i64, _i64, _i64]),
@@ -354,6 +356,14 @@ def make_rope_grid(grid_h, grid_w, origin=(0.0, 0.0, 0.0), step=(1.0, 1.0, 1.0))
 def make_rope_tensors(tensors):
     """tensors: (x, y, x_tok_stride, x_head_stride, y_tok_stride, y_head_stride, heads) each."""
     return (nomas_rope_tensor * max(1, len(tensors)))(*[nomas_rope_tensor(*t, 0) for t in tensors])
+
+
+_ROPE_TENSORS = [struct.Struct("PPqqqqii" * n) for n in range(NOMAS_ROPE_MAX_TENSORS + 1)]
+
+
+def pack_rope_tensors(fields):
+    """The same as packed bytes, from the flat fields (_pad included)."""
+    return _ROPE_TENSORS[len(fields) // 8].pack(*fields)
 
 
 def nomas_rope(spec, grid, positions, tokens, tensors, n_tensors, dtype, inverse, stream=0):

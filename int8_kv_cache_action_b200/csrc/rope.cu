@@ -332,13 +332,14 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
         if (items >= (int64_t)1 << 24) return NOMAS_EUNSUPPORTED;
     }
     if (tokens == 0) return NOMAS_OK;
-    double at = 0.0;
+    // theta^(-2 i / d) as powers of one root: 128 products in the 64-bit mantissa of long double stay exact to fp64
     int pair = 0;
-    for (int a = 0; a < 3; ++a)
-        for (int i = 0; i < spec->axis_dim[a] / 2; ++i, ++pair) {
-            at = std::pow(spec->theta, -2.0 * i / spec->axis_dim[a]);
-            p.turns[pair] = at / 6.283185307179586476925;
-        }
+    for (int a = 0; a < 3; ++a) {
+        if (spec->axis_dim[a] == 0) continue;
+        const long double root = std::pow((long double)spec->theta, -2.0L / spec->axis_dim[a]);
+        long double at = 1.0L / 6.283185307179586476925286766559L;
+        for (int i = 0; i < spec->axis_dim[a] / 2; ++i, at *= root) p.turns[pair++] = (double)at;
+    }
     p.positions = positions;
     p.items = make_fastdiv((uint32_t)items);
     p.per_head = make_fastdiv((uint32_t)per_head);

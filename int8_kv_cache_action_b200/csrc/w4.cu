@@ -3,7 +3,7 @@
 // Kernels:
 //   w4_quantize_kernel  one warp per (row, group)
 //   w4_dequant_kernel   bf16(code * scale), 32 weights per thread (HBM-bound)
-//   w4_rows_kernel      y = x W^T for up to kW4MaxRows rows of x, every code read once: bound by the codes'
+//   w4_rows_kernel      y = x W^T for up to NOMAS_W4_FEW_ROWS rows of x, every code read once: bound by the codes'
 //                       bytes, so the weights are widened in registers and go straight into the register
 //                       form of the tensor-core product (m16n8k16, 16 rows of W by 8 rows of x): one
 //                       instruction per 8 weights of a lane, where fp32 products would need one per
@@ -13,7 +13,6 @@
 
 namespace nomas {
 
-constexpr int kW4MaxRows = 64;
 constexpr int kW4Warps = 8;                    // they share the columns of 16 rows of W
 
 // 8 codes (one word, code i in bits 4i .. 4i + 3) times a scale, as bf16 pairs (i, i + 4), i = 0 .. 3: with
@@ -250,7 +249,7 @@ extern "C" int nomas_w4_dequant(const uint8_t *codes, const void *scales, int gr
 }
 
 extern "C" size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in) {
-    if (m <= kW4MaxRows || n_out < 1 || k_in < 1) return 0;
+    if (m <= NOMAS_W4_FEW_ROWS || n_out < 1 || k_in < 1) return 0;
     return (size_t)n_out * (size_t)k_in * 2;
 }
 
@@ -263,12 +262,12 @@ extern "C" int nomas_w4a16_linear(const void *x, int64_t m, int64_t k_in, int64_
     if (ldx < k_in || ldx % 8 != 0 || ldy < n_out) return NOMAS_EINVAL;
     if (y_dtype != NOMAS_DTYPE_F32 && y_dtype != NOMAS_DTYPE_BF16) return NOMAS_EINVAL;
     if (m >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
-    if (m > kW4MaxRows && (!workspace || !aligned16(workspace))) return NOMAS_EINVAL;
+    if (m > NOMAS_W4_FEW_ROWS && (!workspace || !aligned16(workspace))) return NOMAS_EINVAL;
     if (m == 0) return NOMAS_OK;
     DeviceScope dev(codes);
     if (dev.rc) return dev.rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (m > kW4MaxRows) {
+    if (m > NOMAS_W4_FEW_ROWS) {
         rc = enqueue_w4_dequant(codes, scales, group, n_out, k_in, workspace, st);
         if (rc) return rc;
         return nomas_linear_bf16(x, m, k_in, ldx, workspace, n_out, k_in, y, ldy, y_dtype, status, stream);

@@ -8,6 +8,7 @@ mask build, attention and these operators all run in libnomas's kernels.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 from typing import Optional, Sequence, Tuple
 
@@ -45,33 +46,40 @@ def _token_strides(t: torch.Tensor) -> Tuple[int, int]:
 
 
 def _same_device(ref: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    index = ref.get_device()
     for t in others:
-        if t is not None and t.device != ref.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"tensors on {ref.device} and {t.device}: expected one device")
 
 
 class _on:
-    """Runs a call on the device of `ref`: its current stream, or `stream` (allocations then belong to it)."""
+    """Runs a call on the device of `ref`, on `stream` (allocations then belong to it) or the device's current
+    stream; _stream_on skips it where neither has to change."""
 
-    __slots__ = ("device", "stream", "guards")
+    __slots__ = ("guards",)
 
     def __init__(self, ref: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-        if not ref.is_cuda:
-            raise ValueError(f"expected a CUDA tensor, got one on {ref.device}")
-        self.device, self.stream, self.guards = ref.device, stream, ()
+        if stream is not None and stream.device != ref.device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {ref.device}")
+        self.guards = (torch.cuda.device(ref.device),) + ((torch.cuda.stream(stream),) if stream is not None else ())
 
-    def __enter__(self) -> int:
-        if self.stream is not None:
-            self.guards = (torch.cuda.stream(self.stream),)
-        elif self.device.index != torch.cuda.current_device():
-            self.guards = (torch.cuda.device(self.device),)
+    def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
-        for g in self.guards:
+        for g in reversed(self.guards):
             g.__exit__(*exc)
+
+
+def _stream_on(ref: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> Optional[int]:
+    """The current stream of `ref`'s device as an address, or None when a call needs _on first."""
+    if not ref.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {ref.device}")
+    index = ref.get_device()
+    if stream is not None or index != torch.cuda.current_device():
+        return None
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def segment_text(n_frames: int, head_len: int, tails: Sequence[Tuple[int, int, int]] = ()):
@@ -329,50 +337,67 @@ class Int4Linear:
             raise ValueError("scales: contiguous bfloat16 [N, ceil(K / group)] on the device of codes")
         self.codes, self.scales, self.group = codes, scales, group
         self.status_word = torch.zeros(4, dtype=torch.int32, device=codes.device)
+        self._codes, self._scales, self._status = codes.data_ptr(), scales.data_ptr(), self.status_word.data_ptr()
 
     @classmethod
     def from_weights(cls, w: torch.Tensor, group: int = 64, stream=None) -> "Int4Linear":
         """Quantise bf16 weights [N, K] on the device."""
         if w.dtype != torch.bfloat16 or w.dim() != 2 or w.stride(1) != 1 or w.shape[1] % 32 or group not in (32, 64, 128):
             raise ValueError("w: bf16 [N, K] with contiguous rows, K a multiple of 32; group: 32, 64 or 128")
+        st = _stream_on(w, stream)
+        if st is None:
+            with _on(w, stream):
+                return cls.from_weights(w, group)
         n, k = w.shape
-        with _on(w, stream) as st:
-            codes = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
-            scales = torch.empty((n, -(-k // group)), dtype=torch.bfloat16, device=w.device)
-            N._check(N.nomas_w4_quantize(w.data_ptr(), n, k, w.stride(0), group, codes.data_ptr(), scales.data_ptr(),
-                                         st), "nomas_w4_quantize")
-            return cls(codes, scales, group)
+        codes = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((n, -(-k // group)), dtype=torch.bfloat16, device=w.device)
+        N._check(N.nomas_w4_quantize(w.data_ptr(), n, k, w.stride(0), group, codes.data_ptr(), scales.data_ptr(), st),
+                 "nomas_w4_quantize")
+        return cls(codes, scales, group)
 
     def dequantized(self, stream=None) -> torch.Tensor:
-        with _on(self.codes, stream) as st:
-            w = torch.empty((self.n_out, self.k_in), dtype=torch.bfloat16, device=self.codes.device)
-            N._check(N.nomas_w4_dequant(self.codes.data_ptr(), self.scales.data_ptr(), self.group, self.n_out,
-                                        self.k_in, w.data_ptr(), st), "nomas_w4_dequant")
+        st = _stream_on(self.codes, stream)
+        if st is None:
+            with _on(self.codes, stream):
+                return self.dequantized()
+        w = torch.empty((self.n_out, self.k_in), dtype=torch.bfloat16, device=self.codes.device)
+        N._check(N.nomas_w4_dequant(self.codes.data_ptr(), self.scales.data_ptr(), self.group, self.n_out, self.k_in,
+                                    w.data_ptr(), st), "nomas_w4_dequant")
         return w
 
     def __call__(self, x: torch.Tensor, out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
                  stream=None) -> torch.Tensor:
-        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != self.k_in:
+        st = _stream_on(self.codes, stream)
+        if st is None:
+            with _on(self.codes, stream):
+                return self(x, out_dtype, out)
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.k_in or x.stride(1) != 1:
             raise ValueError("x: bf16 [M, K] with contiguous rows")
         m = x.shape[0]
-        if out is not None and (out.shape != (m, self.n_out) or out.dtype not in _DTYPES or out.stride(1) != 1):
+        if out is None:
+            out = torch.empty((m, self.n_out), dtype=out_dtype, device=x.device)
+        elif out.shape != (m, self.n_out) or out.stride(1) != 1:
+            raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
+        if out.dtype not in _DTYPES:
             raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
         _same_device(self.codes, x, out)
-        with _on(self.codes, stream) as st:
-            if out is None:
-                out = torch.empty((m, self.n_out), dtype=out_dtype, device=x.device)
-            need = N.nomas_w4a16_workspace_bytes(m, self.n_out, self.k_in)
-            ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-            if m:
-                N._check(N.nomas_w4a16_linear(x.data_ptr(), m, self.k_in, _pitch(x), self.codes.data_ptr(),
-                                              self.scales.data_ptr(), self.group, self.n_out, out.data_ptr(),
-                                              _pitch(out), _DTYPES[out.dtype], ws.data_ptr() if need else 0,
-                                              self.status_word.data_ptr(), st), "nomas_w4a16_linear")
+        if m:
+            ws = 0
+            if m > N.NOMAS_W4_FEW_ROWS:
+                keep = torch.empty(N.nomas_w4a16_workspace_bytes(m, self.n_out, self.k_in), dtype=torch.uint8,
+                                   device=x.device)
+                ws = keep.data_ptr()
+            N._check(N.lib.nomas_w4a16_linear(x.data_ptr(), m, self.k_in, _pitch(x), self._codes, self._scales, self.group,
+                                              self.n_out, out.data_ptr(), _pitch(out), _DTYPES[out.dtype], ws,
+                                              self._status, st), "nomas_w4a16_linear")
         return out
 
     def status(self, stream=None) -> int:
-        with _on(self.codes, stream) as st:
-            return N.nomas_status_read(self.status_word.data_ptr(), st)
+        st = _stream_on(self.codes, stream)
+        if st is None:
+            with _on(self.codes, stream):
+                return self.status()
+        return N.nomas_status_read(self._status, st)
 
 
 # ------------------------------------------------------------------------------------------------
@@ -408,34 +433,40 @@ class AxisRope:
         if not 1 <= len(xs) <= N.NOMAS_ROPE_MAX_TENSORS:
             raise ValueError(f"1 to {N.NOMAS_ROPE_MAX_TENSORS} tensors")
         ref = xs[0]
-        if ref.dim() != 3 or ref.dtype not in _DTYPES:
+        st = _stream_on(ref, stream)
+        if st is None:
+            with _on(ref, stream):
+                return self(tensors, grid, positions, inverse, out)
+        dtype = ref.dtype
+        if ref.dim() != 3 or dtype not in _DTYPES:
             raise ValueError("expected bf16 or fp32 [tokens, heads, head_dim] tensors with contiguous head_dim")
         if (grid is None) == (positions is None):
             raise ValueError("give either grid or positions")
-        t = ref.shape[0]
-        if positions is not None and (positions.dtype != torch.float32 or positions.shape != (t, 3) or
-                                      not positions.is_contiguous()):
-            raise ValueError("positions: contiguous fp32 [tokens, 3]")
-        with _on(ref, stream) as st:
-            if out is None:
-                ys = tuple(torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs)
-            else:
-                ys = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-                if len(ys) != len(xs):
-                    raise ValueError("out: one tensor for each input")
-            _same_device(ref, positions, *xs, *ys)
-            args = []
-            for x, y in zip(xs, ys):
-                for v in (x, y):
-                    if v.dtype != ref.dtype or v.dim() != 3 or v.shape[0] != t or v.shape[2] != self.head_dim or \
-                            v.shape[1] != x.shape[1] or v.stride(2) != 1:
-                        raise ValueError("expected tensors [tokens, heads, head_dim] of one type and token count with "
-                                         "contiguous head_dim")
-                args.append((x.data_ptr(), y.data_ptr(), *_token_strides(x), *_token_strides(y), x.shape[1]))
-            if t and all(a[-1] for a in args):
-                N._check(N.nomas_rope(self.spec, grid, positions.data_ptr() if positions is not None else 0, t,
-                                      N.make_rope_tensors(args), len(args), _DTYPES[ref.dtype], inverse, st), "nomas_rope")
-        return ys[0] if single else ys
+        t, device = ref.shape[0], ref.device
+        if positions is not None:
+            if positions.dtype != torch.float32 or positions.shape != (t, 3) or not positions.is_contiguous():
+                raise ValueError("positions: contiguous fp32 [tokens, 3]")
+            _same_device(ref, positions)
+        if out is None:
+            ys = [torch.empty(x.shape, dtype=dtype, device=device) for x in xs]
+        else:
+            ys = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+            if len(ys) != len(xs):
+                raise ValueError("out: one tensor for each input")
+        args = []
+        for x, y in zip(xs, ys):
+            shape = x.shape
+            if len(shape) != 3 or shape[0] != t or shape[2] != self.head_dim or x.dtype != dtype or x.stride(2) != 1 or \
+                    y.shape != shape or y.dtype != dtype or y.stride(2) != 1:
+                raise ValueError("expected tensors [tokens, heads, head_dim] of one type and token count with "
+                                 "contiguous head_dim")
+            _same_device(ref, x, y)
+            args += (x.data_ptr(), y.data_ptr(), *_token_strides(x), *_token_strides(y), shape[1], 0)
+        if t and min(args[6::8]):
+            N._check(N.lib.nomas_rope(ctypes.byref(self.spec), None if grid is None else ctypes.byref(grid),
+                                      0 if positions is None else positions.data_ptr(), t, N.pack_rope_tensors(args),
+                                      len(xs), _DTYPES[dtype], inverse, st), "nomas_rope")
+        return ys[0] if single else tuple(ys)
 
 
 # ------------------------------------------------------------------------------------------------
@@ -443,23 +474,27 @@ class AxisRope:
 # ------------------------------------------------------------------------------------------------
 
 def _norm_params(x, weight, bias, rows_per_group):
-    """(weight, bias, pitch, type, groups) of a layer norm's parameters: [C], or [groups, C]."""
+    """(pitch, type, groups) of a layer norm's parameters: [C], or [groups, C]."""
     if x.dim() != 2 or x.dtype not in _DTYPES or x.stride(1) != 1:
         raise ValueError("x: bf16 or fp32 [rows, C] with contiguous rows")
     rows, cols = x.shape
+    if rows_per_group < 0:
+        raise ValueError("rows_per_group: at least 0")
     groups = -(-rows // rows_per_group) if rows_per_group else 1
-    dtype, pitch = None, None
-    for name, p in (("weight", weight), ("bias", bias)):
+    pitch, dtype = 0, None
+    for p in (weight, bias):
         if p is None:
             continue
-        if p.dtype not in _DTYPES or p.shape not in (((cols,), (1, cols)) if groups == 1 else ((groups, cols),)) or \
-                p.stride(-1) != 1:
-            raise ValueError(f"{name}: bf16 or fp32 [groups, C] ([C] for one group) with contiguous rows")
-        at = p.stride(0) if p.dim() == 2 and groups > 1 else cols
-        if pitch is not None and (at != pitch or p.dtype != dtype):
+        shape, strides = p.shape, p.stride()
+        if len(shape) == 1:
+            shape, strides = (1, *shape), (cols, *strides)
+        if shape != (groups, cols) or p.dtype not in _DTYPES or strides[1] != 1:
+            raise ValueError("weight, bias: bf16 or fp32 [groups, C] ([C] for one group) with contiguous rows")
+        at = strides[0] if groups > 1 else cols
+        if dtype is not None and (at != pitch or p.dtype != dtype):
             raise ValueError("weight and bias must share their type and strides")
-        dtype, pitch = p.dtype, at
-    return pitch or cols, _DTYPES[dtype] if dtype is not None else N.NOMAS_DTYPE_F32, groups
+        pitch, dtype = at, p.dtype
+    return pitch or cols, _DTYPES[dtype or torch.float32], groups
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -469,22 +504,25 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     xhat * (1 + weight) + bias (modulation).  rows_per_group: rows that share a row of weight and bias
     ([groups, C]); 0: one weight and bias [C] for all.  Returns y, or (y, mean, rstd) with want_stats, which
     layer_norm_backward takes."""
-    if rows_per_group < 0:
-        raise ValueError("rows_per_group: at least 0")
+    st = _stream_on(x, stream)
+    if st is None:
+        with _on(x, stream):
+            return layer_norm(x, weight, bias, eps, rows_per_group, unit_offset, out_dtype, out, want_stats)
     pitch, p_dtype, _ = _norm_params(x, weight, bias, rows_per_group)
     rows, cols = x.shape
-    if out is not None and (out.shape != x.shape or out.dtype not in _DTYPES or out.stride(1) != 1):
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape or out.stride(1) != 1:
+        raise ValueError("out: bf16 or fp32 [rows, C] with contiguous rows")
+    if out.dtype not in _DTYPES:
         raise ValueError("out: bf16 or fp32 [rows, C] with contiguous rows")
     _same_device(x, weight, bias, out)
-    with _on(x, stream) as st:
-        if out is None:
-            out = torch.empty((rows, cols), dtype=out_dtype or x.dtype, device=x.device)
-        mean = rstd = None
-        if want_stats:
-            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-        if rows:
-            N._check(N.nomas_layernorm_fwd(x.data_ptr(), rows, cols, _pitch(x), _DTYPES[x.dtype], _ptr(weight), _ptr(bias),
+    mean = rstd = None
+    if want_stats:
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if rows:
+        N._check(N.lib.nomas_layernorm_fwd(x.data_ptr(), rows, cols, _pitch(x), _DTYPES[x.dtype], _ptr(weight), _ptr(bias),
                                            pitch, p_dtype, rows_per_group, unit_offset, eps, out.data_ptr(), _pitch(out),
                                            _DTYPES[out.dtype], _ptr(mean), _ptr(rstd), st), "nomas_layernorm_fwd")
     return (out, mean, rstd) if want_stats else out
@@ -495,8 +533,10 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
                         want_dx: bool = True, want_params: bool = True, stream=None):
     """Gradients of layer_norm: (dx of x's type, dweight fp32 [groups, C], dbias fp32 [groups, C]); what is not
     wanted is None.  mean and rstd are layer_norm's."""
-    if rows_per_group < 0:
-        raise ValueError("rows_per_group: at least 0")
+    st = _stream_on(x, stream)
+    if st is None:
+        with _on(x, stream):
+            return layer_norm_backward(dy, x, mean, rstd, weight, rows_per_group, unit_offset, want_dx, want_params)
     pitch, p_dtype, groups = _norm_params(x, weight, None, rows_per_group)
     rows, cols = x.shape
     if dy.shape != x.shape or dy.dtype not in _DTYPES or dy.stride(1) != 1:
@@ -505,20 +545,18 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
         if s.dtype != torch.float32 or s.shape != (rows,) or not s.is_contiguous():
             raise ValueError("mean, rstd: contiguous fp32 [rows]")
     _same_device(x, dy, mean, rstd, weight)
-    with _on(x, stream) as st:
-        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if want_dx else None
-        dw = db = ws = None
-        if want_params:
-            dw = torch.empty((groups, cols), dtype=torch.float32, device=x.device)
-            db = torch.empty((groups, cols), dtype=torch.float32, device=x.device)
-            ws = torch.empty(N.nomas_layernorm_workspace_bytes(rows, cols, rows_per_group), dtype=torch.uint8,
-                             device=x.device)
-        if rows and (want_dx or want_params):
-            N._check(N.nomas_layernorm_bwd(dy.data_ptr(), _pitch(dy), _DTYPES[dy.dtype], x.data_ptr(), _pitch(x),
+    device = x.device
+    dx = torch.empty((rows, cols), dtype=x.dtype, device=device) if want_dx else None
+    dw = db = ws = None
+    if want_params:
+        dw, db = torch.empty((2, groups, cols), dtype=torch.float32, device=device).unbind()
+        ws = torch.empty(N.lib.nomas_layernorm_workspace_bytes(rows, cols, rows_per_group), dtype=torch.uint8, device=device)
+    if rows and (want_dx or want_params):
+        N._check(N.lib.nomas_layernorm_bwd(dy.data_ptr(), _pitch(dy), _DTYPES[dy.dtype], x.data_ptr(), _pitch(x),
                                            _DTYPES[x.dtype], rows, cols, _ptr(weight), pitch, p_dtype, rows_per_group,
                                            unit_offset, mean.data_ptr(), rstd.data_ptr(), _ptr(dx), cols, _ptr(dw),
                                            _ptr(db), cols, _ptr(ws), st), "nomas_layernorm_bwd")
-        elif want_params:
-            dw.zero_()
-            db.zero_()
+    elif want_params:
+        dw.zero_()
+        db.zero_()
     return dx, dw, db
