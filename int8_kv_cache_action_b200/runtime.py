@@ -40,11 +40,6 @@ def _pitch(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
 
 
-def _token_strides(t: torch.Tensor) -> Tuple[int, int]:
-    """Token and head strides of [tokens, heads, head_dim]; a single token's or head's stride says nothing."""
-    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
-
-
 def _same_device(ref: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
     index = ref.get_device()
     for t in others:
@@ -375,7 +370,7 @@ class Int4Linear:
             raise ValueError("x: bf16 [M, K] with contiguous rows")
         m = x.shape[0]
         if out is None:
-            out = torch.empty((m, self.n_out), dtype=out_dtype, device=x.device)
+            out = x.new_empty((m, self.n_out), dtype=out_dtype)
         elif out.shape != (m, self.n_out) or out.stride(1) != 1:
             raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
         if out.dtype not in _DTYPES:
@@ -422,6 +417,7 @@ class AxisRope:
         self.head_dim = head_dim
         self.spec = N.make_rope_spec(head_dim, axis_dims, theta,
                                      N.NOMAS_ROPE_HALVES if pairing == "halves" else N.NOMAS_ROPE_INTERLEAVED)
+        self._spec = ctypes.byref(self.spec)
 
     def __call__(self, tensors, grid=None, positions: Optional[torch.Tensor] = None, inverse: bool = False, out=None,
                  stream=None):
@@ -442,29 +438,36 @@ class AxisRope:
             raise ValueError("expected bf16 or fp32 [tokens, heads, head_dim] tensors with contiguous head_dim")
         if (grid is None) == (positions is None):
             raise ValueError("give either grid or positions")
-        t, device = ref.shape[0], ref.device
+        t = ref.shape[0]
         if positions is not None:
             if positions.dtype != torch.float32 or positions.shape != (t, 3) or not positions.is_contiguous():
                 raise ValueError("positions: contiguous fp32 [tokens, 3]")
             _same_device(ref, positions)
-        if out is None:
-            ys = [torch.empty(x.shape, dtype=dtype, device=device) for x in xs]
-        else:
-            ys = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-            if len(ys) != len(xs):
-                raise ValueError("out: one tensor for each input")
-        args = []
-        for x, y in zip(xs, ys):
-            shape = x.shape
-            if len(shape) != 3 or shape[0] != t or shape[2] != self.head_dim or x.dtype != dtype or x.stride(2) != 1 or \
-                    y.shape != shape or y.dtype != dtype or y.stride(2) != 1:
-                raise ValueError("expected tensors [tokens, heads, head_dim] of one type and token count with "
+        index, d = ref.get_device(), self.head_dim
+        args, ys = [], []
+        given = (None,) * len(xs) if out is None else (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(given) != len(xs):
+            raise ValueError("out: one tensor for each input")
+        for x, y in zip(xs, given):
+            shape, sx = x.shape, x.stride()
+            if len(shape) != 3 or shape[0] != t or shape[2] != d or x.dtype != dtype or sx[2] != 1 or x.get_device() != index:
+                raise ValueError("expected tensors [tokens, heads, head_dim] of one device, type and token count with "
                                  "contiguous head_dim")
-            _same_device(ref, x, y)
-            args += (x.data_ptr(), y.data_ptr(), *_token_strides(x), *_token_strides(y), shape[1], 0)
+            h = shape[1]
+            if y is None:
+                y = torch.empty_like(x, memory_format=torch.contiguous_format)
+                sy = (h * d, d)
+            else:
+                sy = y.stride()
+                if y.shape != shape or y.dtype != dtype or sy[2] != 1 or y.get_device() != index:
+                    raise ValueError("out: tensors of the inputs' shape, type and device with contiguous head_dim")
+            ys.append(y)
+            # a single token's or head's stride says nothing
+            args += (x.data_ptr(), y.data_ptr(), sx[0] if t > 1 else 0, sx[1] if h > 1 else 0, sy[0] if t > 1 else 0,
+                     sy[1] if h > 1 else 0, h, 0)
         if t and min(args[6::8]):
-            N._check(N.lib.nomas_rope(ctypes.byref(self.spec), None if grid is None else ctypes.byref(grid),
-                                      0 if positions is None else positions.data_ptr(), t, N.pack_rope_tensors(args),
+            N._check(N.lib.nomas_rope(self._spec, None if grid is None else ctypes.byref(grid),
+                                      None if positions is None else positions.data_ptr(), t, N.pack_rope_tensors(args),
                                       len(xs), _DTYPES[dtype], inverse, st), "nomas_rope")
         return ys[0] if single else tuple(ys)
 
@@ -511,7 +514,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     pitch, p_dtype, _ = _norm_params(x, weight, bias, rows_per_group)
     rows, cols = x.shape
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype or x.dtype, device=x.device)
+        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or out.stride(1) != 1:
         raise ValueError("out: bf16 or fp32 [rows, C] with contiguous rows")
     if out.dtype not in _DTYPES:
@@ -519,8 +522,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     _same_device(x, weight, bias, out)
     mean = rstd = None
     if want_stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        mean = x.new_empty(rows, dtype=torch.float32)
+        rstd = torch.empty_like(mean)
     if rows:
         N._check(N.lib.nomas_layernorm_fwd(x.data_ptr(), rows, cols, _pitch(x), _DTYPES[x.dtype], _ptr(weight), _ptr(bias),
                                            pitch, p_dtype, rows_per_group, unit_offset, eps, out.data_ptr(), _pitch(out),
@@ -546,10 +549,11 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
             raise ValueError("mean, rstd: contiguous fp32 [rows]")
     _same_device(x, dy, mean, rstd, weight)
     device = x.device
-    dx = torch.empty((rows, cols), dtype=x.dtype, device=device) if want_dx else None
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dx else None
     dw = db = ws = None
     if want_params:
-        dw, db = torch.empty((2, groups, cols), dtype=torch.float32, device=device).unbind()
+        dw = x.new_empty((groups, cols), dtype=torch.float32)
+        db = torch.empty_like(dw)
         ws = torch.empty(N.lib.nomas_layernorm_workspace_bytes(rows, cols, rows_per_group), dtype=torch.uint8, device=device)
     if rows and (want_dx or want_params):
         N._check(N.lib.nomas_layernorm_bwd(dy.data_ptr(), _pitch(dy), _DTYPES[dy.dtype], x.data_ptr(), _pitch(x),
