@@ -9,7 +9,6 @@
 //                       instruction per 8 weights of a lane, where fp32 products would need one per
 //                       weight and row of x.  tcgen05 would want the widened weights in shared memory
 //                       first; it takes over (w4_dequant_kernel, nomas_linear_bf16) for more rows.
-#include <cstdlib>
 #include "common.cuh"
 
 namespace nomas {
@@ -65,27 +64,34 @@ struct W4Codes {
     __nv_bfloat16 f[RT][2];
 };
 
+// CTAs of an SM, from the warps that the sums of RT * NT products leave registers for.  24 warps spill a little with
+// RT = 2, and pay on wide matrices (2 x 8192 -> 28001: 35.6 us, 43.9 with 20, 45.3 with 16).
 template <int NT, int RT, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) w4_rows_kernel(const W4Params p) {
+constexpr int w4_ctas = (NT * RT <= 2 ? 24 : 16) / WARPS > 0 ? (NT * RT <= 2 ? 24 : 16) / WARPS : 1;
+
+template <int NT, int RT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_kernel(const W4Params p) {
     extern __shared__ float red[];             // [WARPS][8 NT][16 RT + 1]
     constexpr int LD = 16 * RT + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
     const int chunks = p.k >> 7, tail = p.k & 127;
-    const uint8_t *codes[RT][2];
-    const __nv_bfloat16 *scales[RT][2], *xr[NT];
-    const int col0 = warp * 128 + 32 * t;
-    // rows past the end repeat the last one: their products go nowhere
+    // this CTA's rows: 32-bit offsets from the first; rows past the end repeat the last one, and their products go
+    // nowhere
+    const uint8_t *const codes = p.codes + n0 * (p.k / 2), *const scales = reinterpret_cast<const uint8_t *>(p.scales + n0 * p.groups);
+    const uint32_t last = (uint32_t)min((int64_t)(16 * RT), p.n - n0) - 1;
+    uint32_t code_at[RT][2], scale_at[RT][2];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t row = min(n0 + 16 * r + 8 * h + g, p.n - 1);
-            codes[r][h] = p.codes + row * (p.k / 2) + col0 / 2;
-            scales[r][h] = p.scales + row * p.groups;
+            const uint32_t row = min((uint32_t)(16 * r + 8 * h + g), last);
+            code_at[r][h] = row * (p.k / 2) + 16 * t;
+            scale_at[r][h] = row * 2 * p.groups;
         }
+    const __nv_bfloat16 *xr[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) xr[i] = p.x + (int64_t)min(8 * i + g, p.m - 1) * p.ldx + col0;
+    for (int i = 0; i < NT; ++i) xr[i] = p.x + (int64_t)min(8 * i + g, p.m - 1) * p.ldx + 32 * t;
     float acc[RT][NT][4];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -95,15 +101,19 @@ __global__ void __launch_bounds__(32 * WARPS) w4_rows_kernel(const W4Params p) {
             for (int j = 0; j < 4; ++j) acc[r][i][j] = 0.0f;
 
     auto load = [&](W4Codes<RT> &v, int c) {   // chunk c: columns 128 c ..
+        const uint32_t group = (uint32_t)(c * 128 + 32 * t) >> p.group_log2;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                v.w[r][h] = load_stream(codes[r][h] + (c - warp) * 64);
-                v.f[r][h] = scales[r][h][(c * 128 + 32 * t) >> p.group_log2];
+                v.w[r][h] = load_stream(codes + (code_at[r][h] + c * 64));
+                v.f[r][h] = *reinterpret_cast<const __nv_bfloat16 *>(scales + (scale_at[r][h] + 2 * group));
             }
     };
     auto multiply = [&](const W4Codes<RT> &v, int c, bool in) {
+        // the tensor cores truncate sums: short runs of columns are added up in rounded fp32, a whole chunk where its
+        // sums fit the registers, else 32 columns
+        constexpr bool WHOLE = RT * NT <= 2;
         float part[RT][NT][4];
         __nv_bfloat162 s[RT][2];
 #pragma unroll
@@ -128,7 +138,7 @@ __global__ void __launch_bounds__(32 * WARPS) w4_rows_kernel(const W4Params p) {
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 uint4 xv = make_uint4(0, 0, 0, 0);
-                if (in) xv = __ldg(reinterpret_cast<const uint4 *>(xr[i] + (c - warp) * 128 + 8 * q));
+                if (in) xv = __ldg(reinterpret_cast<const uint4 *>(xr[i] + c * 128 + 8 * q));
                 // pairs (0,4) (1,5) (2,6) (3,7) of 8 columns
                 const uint32_t x0 = __byte_perm(xv.x, xv.z, 0x5410), x1 = __byte_perm(xv.x, xv.z, 0x7632);
                 const uint32_t x2 = __byte_perm(xv.y, xv.w, 0x5410), x3 = __byte_perm(xv.y, xv.w, 0x7632);
@@ -136,20 +146,14 @@ __global__ void __launch_bounds__(32 * WARPS) w4_rows_kernel(const W4Params p) {
                 for (int r = 0; r < RT; ++r) {
                     mma_16x8x16(part[r][i], u[r][0][0], u[r][1][0], u[r][0][1], u[r][1][1], x0, x1);
                     mma_16x8x16(part[r][i], u[r][0][2], u[r][1][2], u[r][0][3], u[r][1][3], x2, x3);
-                }
-            }
-            // the tensor cores truncate sums: short runs of columns are added up in rounded fp32 (a whole chunk while
-            // its sums fit the registers)
-            if (q == 3 || RT * NT > 2) {
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
+                    if (q == 3 || !WHOLE) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             acc[r][i][j] += part[r][i][j];
                             part[r][i][j] = 0.0f;
                         }
+                    }
+                }
             }
         }
     };
@@ -184,9 +188,9 @@ __global__ void __launch_bounds__(32 * WARPS) w4_rows_kernel(const W4Params p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) mine[(8 * i + 2 * t + (j & 1)) * LD + 16 * r + 8 * (j >> 1) + g] = acc[r][i][j];
     __syncthreads();
-    for (int e = threadIdx.x; e < NT * 8 * 16 * RT; e += 32 * WARPS) {
+    for (int e = threadIdx.x; e < p.m * 16 * RT; e += 32 * WARPS) {
         const int row = e / (16 * RT), col = e % (16 * RT);
-        if (row >= p.m || n0 + col >= p.n) continue;
+        if (n0 + col >= p.n) continue;
         float s = red[row * LD + col];
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) s += red[(w * 8 * NT + row) * LD + col];
@@ -195,198 +199,6 @@ __global__ void __launch_bounds__(32 * WARPS) w4_rows_kernel(const W4Params p) {
         else
             static_cast<float *>(p.y)[(int64_t)row * p.ldy + n0 + col] = s;
     }
-}
-
-// The same with x resident: the CTA holds all of x in shared memory, in the order in which lanes take it, and walks
-// over tiles of rows of W; its warps are wk columns by WARPS / wk rows of 16 RT.  Every thread copies the codes it
-// will widen itself, kW4Stages - 1 steps (chunks of its warp, over all tiles) ahead, through a ring of its own in shared
-// memory; scales come one step ahead.
-constexpr int kW4Stages = 4;
-
-struct W4Resident {
-    W4Params p;
-    int32_t wk_log2, x_pitch;                  // x_pitch: bytes of a row of x in shared memory
-    uint32_t tiles;
-};
-
-template <int NT, int RT>
-constexpr int w4_buffers = NT * RT <= 4 ? 2 : 1;
-
-template <int NT, int RT, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? (RT * NT == 1 ? 3 : 2) : 1) w4_resident_kernel(const W4Resident a) {
-    constexpr int S = kW4Stages, T = 32 * WARPS, LD = 16 * RT + 1, BUFFERS = w4_buffers<NT, RT>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    const W4Params &p = a.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int wk = 1 << a.wk_log2, kw = warp & (wk - 1), rw = warp >> a.wk_log2;
-    const int tile_rows = (16 * RT * WARPS) >> a.wk_log2, chunks = (p.k + 127) >> 7;
-    const uint32_t ring_at = smem_u32(smem) + threadIdx.x * 16;
-    uint8_t *const xs = smem + S * RT * 2 * T * 16;
-    float *const red = reinterpret_cast<float *>(xs + p.m * a.x_pitch);     // [BUFFERS][WARPS][8 NT][LD]
-
-    // the rows of W that this lane widens (g + 8 h of the warp's r-th 16; rows past the end repeat the last one), as
-    // 32-bit byte offsets: codes for the tile being fetched, scales for the tile of the next step
-    auto rows_of = [&](uint32_t tile, uint32_t pitch, uint32_t (&at)[RT][2]) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                at[r][h] = min(tile * tile_rows + rw * (16 * RT) + 16 * r + 8 * h + g, (uint32_t)p.n - 1) * pitch;
-    };
-    uint32_t fetch_tile = blockIdx.x, code_at[RT][2], scale_at[RT][2];
-    int fetch_c = kw;
-    rows_of(fetch_tile, p.k / 2, code_at);
-    rows_of(fetch_tile, 2 * p.groups, scale_at);
-    auto fetch = [&](int stage) {
-        if (fetch_tile < a.tiles) {
-            const int col = fetch_c * 128 + 32 * t, n = col < p.k ? 16 : 0;
-            const uint32_t off = n ? col / 2 : 0;
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring_at + ((stage * RT + r) * 2 + h) * T * 16),
-                                 "l"(p.codes + (code_at[r][h] + off)), "r"(n)
-                                 : "memory");
-            fetch_c += wk;
-            if (fetch_c >= chunks) {
-                fetch_c = kw;
-                fetch_tile += gridDim.x;
-                rows_of(fetch_tile, p.k / 2, code_at);
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) fetch(i);
-
-    // x: 8 columns 128 c + 32 t + 8 q .. of a row as pairs (0,4) (1,5) (2,6) (3,7), 16 bytes at ((c * 4 + q) * 4 + t)
-    for (int row = 0; row < p.m; ++row)
-        for (int e = threadIdx.x; e < chunks * 16; e += T) {
-            const int col = (e >> 4) * 128 + (e & 3) * 32 + ((e >> 2) & 3) * 8;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (col < p.k) v = __ldg(reinterpret_cast<const uint4 *>(p.x + (int64_t)row * p.ldx + col));
-            *reinterpret_cast<uint4 *>(xs + row * a.x_pitch + e * 16) =
-                make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                           __byte_perm(v.y, v.w, 0x7632));
-        }
-    const uint8_t *xr[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) xr[i] = xs + min(8 * i + g, p.m - 1) * a.x_pitch + t * 16;
-
-    __nv_bfloat16 next_f[RT][2];
-    auto next_scales = [&](int c) {
-        const int col = c * 128 + 32 * t;
-        const uint32_t off = 2 * (col >> p.group_log2);
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                next_f[r][h] = col < p.k ? *reinterpret_cast<const __nv_bfloat16 *>(
-                                               reinterpret_cast<const uint8_t *>(p.scales) + (scale_at[r][h] + off))
-                                         : __float2bfloat16_rn(0.0f);
-    };
-    next_scales(kw);
-    __syncthreads();
-
-    int stage = 0, buffer = 0;
-    for (uint32_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-        float acc[RT][NT][4];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[r][i][j] = 0.0f;
-        for (int c = kw; c < chunks; c += wk) {
-            fetch((stage + S - 1) % S);
-            __nv_bfloat162 s[RT][2];
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) s[r][h] = __halves2bfloat162(next_f[r][h], next_f[r][h]);
-            if (c + wk < chunks) {
-                next_scales(c + wk);
-            } else {
-                rows_of(tile + gridDim.x, 2 * p.groups, scale_at);
-                next_scales(kw);
-            }
-            asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-            uint4 w[RT][2];
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    w[r][h] = *reinterpret_cast<const uint4 *>(smem + ((stage * RT + r) * 2 + h) * T * 16 + threadIdx.x * 16);
-            stage = (stage + 1) % S;
-            float part[RT][NT][4];
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) part[r][i][j] = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t u[RT][2][4];
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        w4_widen(q == 0 ? w[r][h].x : q == 1 ? w[r][h].y : q == 2 ? w[r][h].z : w[r][h].w, s[r][h], u[r][h]);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const uint4 xv = *reinterpret_cast<const uint4 *>(xr[i] + (c * 4 + q) * 64);
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        mma_16x8x16(part[r][i], u[r][0][0], u[r][1][0], u[r][0][1], u[r][1][1], xv.x, xv.y);
-                        mma_16x8x16(part[r][i], u[r][0][2], u[r][1][2], u[r][0][3], u[r][1][3], xv.z, xv.w);
-                    }
-                }
-                // the tensor cores truncate sums: short runs of columns are added up in rounded fp32 (a whole chunk
-                // while its sums fit the registers)
-                if (q == 3 || RT * NT > 2) {
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-#pragma unroll
-                        for (int i = 0; i < NT; ++i)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                acc[r][i][j] += part[r][i][j];
-                                part[r][i][j] = 0.0f;
-                            }
-                }
-            }
-        }
-        // acc: rows g and g + 8 of W, rows 8 i + 2 t and 8 i + 2 t + 1 of x; with two buffers one barrier of the warps
-        // that share rows is enough
-        float *all = red + (buffer * WARPS + (rw << a.wk_log2)) * 8 * NT * LD, *mine = all + kw * 8 * NT * LD;
-        if (BUFFERS == 2) buffer ^= 1;
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mine[(8 * i + 2 * t + (j & 1)) * LD + 16 * r + 8 * (j >> 1) + g] = acc[r][i][j];
-        if (wk == 1)
-            __syncwarp();
-        else
-            named_bar_sync(1 + rw, 32 * wk);
-        const int64_t n0 = (int64_t)tile * tile_rows + rw * (16 * RT);
-        for (int e = kw * 32 + lane; e < p.m * 16 * RT; e += 32 * wk) {
-            const int row = e / (16 * RT), col = e % (16 * RT);
-            if (n0 + col >= p.n) continue;
-            float sum = all[row * LD + col];
-            for (int w = 1; w < wk; ++w) sum += all[(w * 8 * NT + row) * LD + col];
-            if (p.y_bf16)
-                static_cast<__nv_bfloat16 *>(p.y)[(int64_t)row * p.ldy + n0 + col] = __float2bfloat16_rn(sum);
-            else
-                static_cast<float *>(p.y)[(int64_t)row * p.ldy + n0 + col] = sum;
-        }
-        if (BUFFERS == 1 && wk > 1) named_bar_sync(1 + rw, 32 * wk);
-        if (BUFFERS == 1 && wk == 1) __syncwarp();
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 __global__ void __launch_bounds__(256) w4_dequant_kernel(const uint8_t *codes, const __nv_bfloat16 *scales, int64_t total32,
@@ -471,51 +283,22 @@ static int enqueue_w4_dequant(const uint8_t *codes, const void *scales, int grou
 template <int NT, int RT, int WARPS>
 static int launch_w4_rows(const W4Params &p, cudaStream_t st) {
     constexpr int kBytes = WARPS * 8 * NT * (16 * RT + 1) * (int)sizeof(float);
-    static_assert(kBytes <= 48 * 1024, "no opt-in");
+    static_assert(kBytes <= 48 * 1024, "above 48 KB a kernel needs an attribute");
     w4_rows_kernel<NT, RT, WARPS><<<(unsigned)((p.n + 16 * RT - 1) / (16 * RT)), 32 * WARPS, kBytes, st>>>(p);
     return check_launch("w4_rows_kernel launch");
 }
 
-template <int NT, int RT>
-static int pick_w4_warps(const W4Params &p, int warps, cudaStream_t st) {
-    if (warps == 4) return launch_w4_rows<NT, RT, 4>(p, st);
-    if constexpr (NT * RT <= 4) {
-        if (warps == 16) return launch_w4_rows<NT, RT, 16>(p, st);
-    }
-    if constexpr (NT * RT <= 8) return launch_w4_rows<NT, RT, 8>(p, st);
-    return launch_w4_rows<NT, RT, 4>(p, st);
-}
-
-template <int NT, int RT, int WARPS>
-static int launch_w4_resident(const W4Params &p, int wk_log2, cudaStream_t st) {
-    W4Resident a{};
-    a.p = p;
-    a.wk_log2 = wk_log2;
-    a.x_pitch = ((p.k + 127) / 128) * 256 + 64;         // neighbouring rows 64 bytes apart in the banks
-    const int rows = (16 * RT * WARPS) >> wk_log2;
-    a.tiles = (uint32_t)((p.n + rows - 1) / rows);
-    const int64_t bytes = (int64_t)kW4Stages * RT * 2 * 32 * WARPS * 16 + (int64_t)p.m * a.x_pitch +
-                          w4_buffers<NT, RT> * WARPS * 8 * NT * (16 * RT + 1) * (int64_t)sizeof(float);
-    auto kernel = w4_resident_kernel<NT, RT, WARPS>;
-    if (bytes > 224 * 1024 || (1 << wk_log2) > WARPS) return launch_w4_rows<NT, NT * RT <= 8 ? RT : 1, 8>(p, st);
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    int64_t ctas = (int64_t)sm_count() * (WARPS == 8 && bytes <= 112 * 1024 ? (RT * NT == 1 && bytes <= 74 * 1024 ? 3 : 2) : 1);
-    if (ctas > a.tiles) ctas = a.tiles;
-    kernel<<<(unsigned)ctas, 32 * WARPS, (size_t)bytes, st>>>(a);
-    return check_launch("w4_resident_kernel launch");
-}
-
+// 32 rows of W a CTA of 4 warps when that gives every SM two CTAs (x is read half as often); narrower matrices take 16
+// rows and split long rows over more warps, so that the codes on their way still fill the machine (5 x 8192 -> 2048:
+// 6.0 us with 16 warps, 6.9 with 8, 9.9 with 4; 1 x 2048 -> 12288: 6.0 with 4, 6.7 with 8; with 32 rows and 4 warps 13.5
+// and 6.3).
 template <int NT>
 static int pick_w4_rows(const W4Params &p, cudaStream_t st) {
-    static const int rt = getenv("W4RT") ? atoi(getenv("W4RT")) : 2, warps = getenv("W4W") ? atoi(getenv("W4W")) : 8;
-    static const int wk = getenv("W4K") ? atoi(getenv("W4K")) : 3;
     if constexpr (NT <= 4) {
-        if (wk >= 0) {
-            if (warps == 16) return rt == 1 ? launch_w4_resident<NT, 1, 16>(p, wk, st) : launch_w4_resident<NT, 2, 16>(p, wk, st);
-            return rt == 1 ? launch_w4_resident<NT, 1, 8>(p, wk, st) : launch_w4_resident<NT, 2, 8>(p, wk, st);
-        }
+        if (p.n >= 64 * (int64_t)sm_count()) return launch_w4_rows<NT, 2, 4>(p, st);
+        if (p.k >= 4096) return launch_w4_rows<NT, 1, 16>(p, st);
     }
-    return rt == 1 ? pick_w4_warps<NT, 1>(p, warps, st) : pick_w4_warps<NT, 2>(p, warps, st);
+    return p.k >= 2048 ? launch_w4_rows<NT, 1, 8>(p, st) : launch_w4_rows<NT, 1, 4>(p, st);
 }
 
 }  // namespace nomas
