@@ -14,19 +14,18 @@ namespace nomas {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeUnroll = 4;                 // 16-byte chunks (chunk pairs) in flight per thread
-constexpr int kRopeTable = 2048;               // (cos, sin) entries of a CTA's tokens: 16 KB
+constexpr int kRopeTable = 4096;               // (cos, sin) entries of a CTA's tokens: 32 KB
 constexpr int kRopeMaxPairs = NOMAS_ROPE_MAX_HEAD_DIM / 2;
 
-// How a 16-byte chunk finds the other value of its pairs: in itself (interleaved), in a second chunk that
-// the same thread holds (halves, where every axis' half is whole chunks), or anywhere in its row, through
-// shared memory (halves of other widths).
-enum RopeForm { kRopeInside = 0, kRopeTwoChunks = 1, kRopeGather = 2 };
+// How a pair's values are reached: in one 16-byte chunk (interleaved), in two that the same thread holds (halves,
+// where every axis' half is whole chunks), or one by one (halves of other widths: rope_pairs_kernel).
+enum RopeForm { kRopeInside = 0, kRopeTwoChunks = 1, kRopePairs = 2 };
 
 struct RopeTensor {
     const char *x;
     char *y;
     int64_t x_tok, x_head, y_tok, y_head;      // bytes
-    uint32_t first_item;                       // items of a token in front of this tensor's
+    uint32_t first_item, first_row;            // items and rows (heads) of a token in front of this tensor's
 };
 
 struct RopeParams {
@@ -37,7 +36,8 @@ struct RopeParams {
     FastDiv plane, width;                      // grid_h * grid_w, grid_w
     FastDiv items;                             // items of a token, all tensors
     FastDiv per_head;                          // items of a head
-    uint32_t tokens, tokens_per_cta, batch;    // batch: items that a CTA takes at a time
+    uint32_t tokens, tokens_per_cta, batch;    // batch: items that a CTA takes at a time (pairs: rows of a warp)
+    uint32_t all_rows;                         // rows of a token
     int32_t n_tensors, inverse;
     int32_t axis_at[4];                        // first channel of each axis, end of the last
     int32_t pairs, all_pairs;                  // pairs that turn, head_dim / 2
@@ -127,26 +127,29 @@ __device__ __forceinline__ void rope_two(const RopeParams &p, uint32_t j, uint32
     }
 }
 
-// The table of a CTA's tokens: (cos, sin) of each pair, sin negated for the inverse.
+// (cos, sin) of pair i at a token, sin negated for the inverse.
+__device__ __forceinline__ float2 rope_angle(const RopeParams &p, uint32_t token, int i) {
+    const int a = 2 * i < p.axis_at[1] ? 0 : 2 * i < p.axis_at[2] ? 1 : 2;
+    double at;
+    if (p.positions) {
+        at = (double)__ldg(p.positions + 3 * (int64_t)token + a);
+    } else {
+        const uint32_t f = fdiv(token, p.plane), in = token - f * p.plane.d;
+        const uint32_t row = fdiv(in, p.width), col = in - row * p.width.d;
+        at = fma(p.step[a], (double)(a == 0 ? f : a == 1 ? row : col), p.origin[a]);
+    }
+    // the angle in turns, its whole turns dropped in fp64: what is left keeps fp32's relative precision
+    const double turns = at * p.turns[i];
+    float s, c;
+    sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+    return make_float2(c, p.inverse ? -s : s);
+}
+
+// The table of a CTA's tokens.
 __device__ __forceinline__ void rope_table(const RopeParams &p, uint32_t token0, uint32_t n, float2 *table) {
-    const uint32_t pairs = p.pairs;
     for (uint32_t e = threadIdx.x; e < n * p.all_pairs; e += kRopeThreads) {
         const uint32_t tok = e / (uint32_t)p.all_pairs, i = e - tok * p.all_pairs;
-        if (i >= pairs) continue;              // passes through: never read
-        const int a = 2 * (int)i < p.axis_at[1] ? 0 : 2 * (int)i < p.axis_at[2] ? 1 : 2;
-        double at;
-        if (p.positions) {
-            at = (double)__ldg(p.positions + 3 * (int64_t)(token0 + tok) + a);
-        } else {
-            const uint32_t f = fdiv(token0 + tok, p.plane), in = token0 + tok - f * p.plane.d;
-            const uint32_t row = fdiv(in, p.width), col = in - row * p.width.d;
-            at = fma(p.step[a], (double)(a == 0 ? f : a == 1 ? row : col), p.origin[a]);
-        }
-        // the angle in turns, its whole turns dropped in fp64: what is left keeps fp32's relative precision
-        const double turns = at * p.turns[i];
-        float s, c;
-        sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-        table[e] = make_float2(c, p.inverse ? -s : s);
+        if (i < (uint32_t)p.pairs) table[e] = rope_angle(p, token0 + tok, i);   // others are never read
     }
 }
 
@@ -160,10 +163,6 @@ template <typename T, int FORM>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int V = Chunk<T>::V, U = kRopeUnroll;
     __shared__ __align__(16) float2 table[kRopeTable];
-    __shared__ __align__(16) uint4 rows[FORM == kRopeGather ? U * kRopeThreads : 1];
-    __shared__ int16_t pair_of[FORM == kRopeGather ? NOMAS_ROPE_MAX_HEAD_DIM : 1];      // -1: passes through
-    __shared__ int16_t other_of[FORM == kRopeGather ? NOMAS_ROPE_MAX_HEAD_DIM : 1];     // channel of the pair's other value
-
     const uint32_t token0 = blockIdx.x * p.tokens_per_cta;
     const uint32_t n = min(p.tokens_per_cta, p.tokens - token0);
     const uint32_t items = n * p.items.d;
@@ -191,25 +190,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         }
         if (base == 0) {
             rope_table(p, token0, n, table);
-            if constexpr (FORM == kRopeGather) {
-                for (int c = threadIdx.x; c < 2 * p.all_pairs; c += kRopeThreads) {
-                    int pair = -1, other = c;
-                    for (int a = 0; a < 3; ++a) {
-                        const int s = p.axis_at[a], e = p.axis_at[a + 1], half = (e - s) / 2;
-                        if (c < s || c >= e) continue;
-                        const bool second = c - s >= half;
-                        pair = s / 2 + (c - s) - (second ? half : 0);
-                        other = second ? c - half : c + half;
-                    }
-                    pair_of[c] = (int16_t)pair;
-                    other_of[c] = (int16_t)other;
-                }
-            }
-            __syncthreads();
-        }
-        if constexpr (FORM == kRopeGather) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) rows[u * kRopeThreads + threadIdx.x] = v0[u];
             __syncthreads();
         }
 #pragma unroll
@@ -225,7 +205,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 for (int i = 0; i < V / 2; ++i)
                     if (i0 + i < p.pairs) turn(a[2 * i], a[2 * i + 1], cs[i0 + i]);
                 *reinterpret_cast<uint4 *>(item[u].y) = keep_behind<V>(pack(a), v0[u], 2 * (p.pairs - i0));
-            } else if constexpr (FORM == kRopeTwoChunks) {
+            } else {
                 const int i0 = item[u].j * V;
                 float b[V];
                 unpack(v1[u], b);
@@ -237,31 +217,99 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                 }
                 *reinterpret_cast<uint4 *>(item[u].y) = v0[u];
                 *reinterpret_cast<uint4 *>(item[u].y + apart[u] * sizeof(T)) = v1[u];
-            } else {
-                const T *row = reinterpret_cast<const T *>(rows + (it - base - item[u].j));
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int c = item[u].j * V + i, pair = pair_of[c], other = other_of[c];
-                    if (pair < 0) continue;
-                    const float2 t = cs[pair];
-                    const float o = (float)row[other];
-                    a[i] = other > c ? fmaf(a[i], t.x, -(o * t.y)) : fmaf(o, t.y, a[i] * t.x);
-                }
-                *reinterpret_cast<uint4 *>(item[u].y) = keep_behind<V>(pack(a), v0[u], 2 * p.pairs - (int)item[u].j * V);
             }
         }
-        if constexpr (FORM == kRopeGather) __syncthreads();
     }
+}
+
+// Pairs one by one: a lane holds pairs lane, lane + 32, .. of a head, whose channels and angle stay in registers for
+// `rows` rows (heads) of a token; behind the axes it holds neighbouring channels, which pass through.  Element loads
+// and stores, whole rows of a warp contiguous; a lane writes what it read, so in place is safe.
+template <typename T>
+__device__ __forceinline__ float value_of(T v) { return (float)v; }
+template <typename T>
+__device__ __forceinline__ T rounded(float v);
+template <>
+__device__ __forceinline__ float rounded<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <typename T, int NP>
+__global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int U = NP <= 2 ? 4 : 2;         // rows in flight
+    const uint32_t item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const uint32_t token = fdiv(item, p.items), part = item - token * p.items.d;
+    if (token >= p.tokens) return;
+    uint32_t c1[NP], c2[NP];
+    float2 cs[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const int i = lane + 32 * k;
+        c1[k] = 2 * i, c2[k] = 2 * i + 1;
+        cs[k] = make_float2(1.0f, 0.0f);
+        if (i >= p.pairs) continue;
+        cs[k] = rope_angle(p, token, i);
+#pragma unroll
+        for (int a = 0; a < 3; ++a) {
+            const int s = p.axis_at[a], e = p.axis_at[a + 1];
+            if (2 * i >= s && 2 * i < e) {
+                c1[k] = s / 2 + i;
+                c2[k] = c1[k] + (e - s) / 2;
+            }
+        }
+    }
+    const uint32_t first = part * p.batch, last = min(first + p.batch, p.all_rows);
+    for (uint32_t r0 = first; r0 < last; r0 += U) {
+        T a[U][NP], b[U][NP];
+        T *to[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t row = min(r0 + u, last - 1);
+            int t = 0;
+#pragma unroll
+            for (int i = 1; i < NOMAS_ROPE_MAX_TENSORS; ++i)
+                if (i < p.n_tensors && row >= p.t[i].first_row) t = i;
+            const uint32_t head = row - p.t[t].first_row;
+            const T *x = reinterpret_cast<const T *>(p.t[t].x + token * p.t[t].x_tok + head * p.t[t].x_head);
+            to[u] = reinterpret_cast<T *>(p.t[t].y + token * p.t[t].y_tok + head * p.t[t].y_head);
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                if ((int)lane + 32 * k < p.all_pairs) a[u][k] = x[c1[k]], b[u][k] = x[c2[k]];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r0 + u >= last) break;
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                if ((int)lane + 32 * k >= p.all_pairs) continue;
+                if ((int)lane + 32 * k < p.pairs) {
+                    float v = value_of(a[u][k]), w = value_of(b[u][k]);
+                    turn(v, w, cs[k]);
+                    a[u][k] = rounded<T>(v), b[u][k] = rounded<T>(w);
+                }
+                to[u][c1[k]] = a[u][k], to[u][c2[k]] = b[u][k];
+            }
+        }
+    }
+}
+
+template <typename T>
+static int launch_rope_pairs(unsigned grid, const RopeParams &p, cudaStream_t st) {
+    if (p.all_pairs <= 32)
+        rope_pairs_kernel<T, 1><<<grid, kRopeThreads, 0, st>>>(p);
+    else if (p.all_pairs <= 64)
+        rope_pairs_kernel<T, 2><<<grid, kRopeThreads, 0, st>>>(p);
+    else
+        rope_pairs_kernel<T, 4><<<grid, kRopeThreads, 0, st>>>(p);
+    return check_launch("rope_pairs_kernel launch");
 }
 
 template <typename T>
 static int launch_rope(RopeForm form, unsigned grid, const RopeParams &p, cudaStream_t st) {
     if (form == kRopeInside)
         rope_kernel<T, kRopeInside><<<grid, kRopeThreads, 0, st>>>(p);
-    else if (form == kRopeTwoChunks)
-        rope_kernel<T, kRopeTwoChunks><<<grid, kRopeThreads, 0, st>>>(p);
     else
-        rope_kernel<T, kRopeGather><<<grid, kRopeThreads, 0, st>>>(p);
+        rope_kernel<T, kRopeTwoChunks><<<grid, kRopeThreads, 0, st>>>(p);
     return check_launch("rope_kernel launch");
 }
 
@@ -311,9 +359,9 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
     p.all_pairs = spec->head_dim / 2;
     RopeForm form = kRopeInside;
     if (spec->pairing == NOMAS_ROPE_HALVES) {
-        form = spec->head_dim % (2 * v) == 0 ? kRopeTwoChunks : kRopeGather;
+        form = spec->head_dim % (2 * v) == 0 ? kRopeTwoChunks : kRopePairs;
         for (int a = 0; a < 3; ++a)
-            if (spec->axis_dim[a] % (2 * v) != 0) form = kRopeGather;
+            if (spec->axis_dim[a] % (2 * v) != 0) form = kRopePairs;
     }
     const int64_t per_head = spec->head_dim / (form == kRopeTwoChunks ? 2 * v : v);
     int64_t items = 0;
@@ -327,7 +375,8 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
             return NOMAS_EINVAL;
         if (t.x == t.y && (t.x_tok_stride != t.y_tok_stride || t.x_head_stride != t.y_head_stride)) return NOMAS_EINVAL;
         p.t[i] = RopeTensor{static_cast<const char *>(t.x), static_cast<char *>(t.y), t.x_tok_stride * esize,
-                            t.x_head_stride * esize, t.y_tok_stride * esize, t.y_head_stride * esize, (uint32_t)items};
+                            t.x_head_stride * esize, t.y_tok_stride * esize, t.y_head_stride * esize, (uint32_t)items, p.all_rows};
+        p.all_rows += (uint32_t)t.heads;
         items += t.heads * per_head;
         if (items >= (int64_t)1 << 24) return NOMAS_EUNSUPPORTED;
     }
@@ -355,11 +404,20 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
     if (per_cta > spread) per_cta = spread;
     if (per_cta < 1) per_cta = 1;
     p.tokens_per_cta = (uint32_t)per_cta;
-    // whole head rows a round: the gather form reads a row's other chunks
-    p.batch = (uint32_t)(round / per_head * per_head);
+    p.batch = (uint32_t)round;
     DeviceScope dev(tensors[0].x);
     if (dev.rc) return dev.rc;
-    const unsigned ctas = (unsigned)((tokens + per_cta - 1) / per_cta);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (form == kRopePairs) {
+        // rows that share a token's angles: 32, fewer while there would be fewer than 16 warps an SM
+        p.batch = 32;
+        while (p.batch > 4 && tokens * ((p.all_rows + p.batch - 1) / p.batch) < (int64_t)16 * sm_count()) p.batch /= 2;
+        const int64_t parts = (p.all_rows + p.batch - 1) / p.batch, warps = tokens * parts;
+        if (warps >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
+        p.items = make_fastdiv((uint32_t)parts);
+        const unsigned grid = (unsigned)((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
+        return dtype == NOMAS_DTYPE_BF16 ? launch_rope_pairs<__nv_bfloat16>(grid, p, st) : launch_rope_pairs<float>(grid, p, st);
+    }
+    const unsigned ctas = (unsigned)((tokens + per_cta - 1) / per_cta);
     return dtype == NOMAS_DTYPE_BF16 ? launch_rope<__nv_bfloat16>(form, ctas, p, st) : launch_rope<float>(form, ctas, p, st);
 }
