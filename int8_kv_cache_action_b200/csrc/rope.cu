@@ -2,18 +2,19 @@
 // projection and the append / attention.
 //
 // A call reads and writes every value once and is bound by HBM: 3 flops a value against 2 x 2 bytes.
-// What a token's heads share is its D / 2 sines and cosines, so a CTA takes all heads of a few tokens,
-// issues its loads first, computes the tokens' table while they are in flight (one fp64 product and
-// reduction and one fp32 sincospi per pair: 64 for 2 x 16 x 128 values of q and k) and reads it from
-// shared memory.  No table in global memory, so nothing to keep between calls.
+// What a token's heads share is its D / 2 sines and cosines, so a CTA takes all heads (or 512 chunks of them) of some
+// tokens, issues its first loads, computes the tokens' table while they are in flight and reads it from shared memory.
+// No table in global memory, so nothing to keep between calls.  A thread keeps its chunk of its head from token to
+// token, so that an item costs little more than its arithmetic (with the chunk, head and tensor worked out per item,
+// about 100 instructions each, 26400 tokens of 2 x 16 x 128 took 80 us).
 #include <cmath>
+#include <cstring>
 
 #include "common.cuh"
 
 namespace nomas {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;                 // 16-byte chunks (chunk pairs) in flight per thread
 constexpr int kRopeTable = 4096;               // (cos, sin) entries of a CTA's tokens: 32 KB
 constexpr int kRopeMaxPairs = NOMAS_ROPE_MAX_HEAD_DIM / 2;
 
@@ -28,16 +29,23 @@ struct RopeTensor {
     uint32_t first_item, first_row;            // items and rows (heads) of a token in front of this tensor's
 };
 
+// What a pair's angle in turns is made of: for the grid the turns at index 0 and per index, in 2^-64, whose overflow
+// drops whole turns exactly; for given positions `origin` holds the bits of the fp64 turns per unit.
+struct __align__(16) RopePair {
+    int64_t origin, step;
+};
+
 struct RopeParams {
-    double turns[kRopeMaxPairs];               // turns per unit of position, by pair
-    double origin[3], step[3];
+    RopePair pair[kRopeMaxPairs];
     RopeTensor t[NOMAS_ROPE_MAX_TENSORS];
     const float *positions;                    // or null: the grid
     FastDiv plane, width;                      // grid_h * grid_w, grid_w
-    FastDiv items;                             // items of a token, all tensors
+    FastDiv items;                             // items of a token, all tensors (rope_pairs_kernel: its warps a token)
     FastDiv per_head;                          // items of a head
-    uint32_t tokens, tokens_per_cta, batch;    // batch: items that a CTA takes at a time (pairs: rows of a warp)
-    uint32_t all_rows;                         // rows of a token
+    FastDiv per_token;                         // pairs of a head (all_pairs)
+    uint32_t tokens, tokens_per_cta;
+    uint32_t abreast;                          // tokens that the CTA's threads hold side by side
+    uint32_t all_rows, rows_per_warp, warp_items;      // rope_pairs_kernel: rows of a token, of a warp; (token, rows) items
     int32_t n_tensors, inverse;
     int32_t axis_at[4];                        // first channel of each axis, end of the last
     int32_t pairs, all_pairs;                  // pairs that turn, head_dim / 2
@@ -84,30 +92,6 @@ __device__ __forceinline__ uint4 keep_behind(uint4 out, const uint4 &in, int tur
     return out;
 }
 
-// Where an item (one chunk, or the first of two) is read and written.
-struct RopeItem {
-    const char *x;
-    char *y;
-    uint32_t token, j;                         // token of the CTA, item of the head
-};
-
-__device__ __forceinline__ RopeItem rope_item(const RopeParams &p, uint32_t it, uint32_t token0) {
-    RopeItem r;
-    r.token = fdiv(it, p.items);
-    const uint32_t rest = it - r.token * p.items.d;
-    int k = 0;
-#pragma unroll
-    for (int i = 1; i < NOMAS_ROPE_MAX_TENSORS; ++i)
-        if (i < p.n_tensors && rest >= p.t[i].first_item) k = i;
-    const RopeTensor &t = p.t[k];
-    const uint32_t in = rest - t.first_item, head = fdiv(in, p.per_head);
-    r.j = in - head * p.per_head.d;
-    const int64_t tok = (int64_t)token0 + r.token;
-    r.x = t.x + tok * t.x_tok + (int64_t)head * t.x_head;
-    r.y = t.y + tok * t.y_tok + (int64_t)head * t.y_head;
-    return r;
-}
-
 // First channel of item j in the two-chunk form, and how far its second chunk is: item j holds pairs
 // j V .. j V + V - 1, whose axis starts at channel axis_at[a] = 2 x (pairs in front of it).  Behind the axes
 // the item is two neighbouring chunks that pass through.
@@ -127,30 +111,28 @@ __device__ __forceinline__ void rope_two(const RopeParams &p, uint32_t j, uint32
     }
 }
 
-// (cos, sin) of pair i at a token, sin negated for the inverse.
-__device__ __forceinline__ float2 rope_angle(const RopeParams &p, uint32_t token, int i) {
-    const int a = 2 * i < p.axis_at[1] ? 0 : 2 * i < p.axis_at[2] ? 1 : 2;
-    double at;
+// Lanes hold different pairs, and reading the call's arguments by lane takes one access a lane: it is done once a CTA
+// or warp, never once a token (26400 tokens of one head: 34 us when it was, 12 us).
+__device__ __forceinline__ int rope_axis(const RopeParams &p, int i) {
+    return 2 * i < p.axis_at[1] ? 0 : 2 * i < p.axis_at[2] ? 1 : 2;
+}
+
+// (cos, sin) of a pair at a token, sin negated for the inverse.  What is left of the angle after its whole turns are
+// dropped keeps fp32's relative precision.
+__device__ __forceinline__ float2 rope_angle(const RopeParams &p, const RopePair &r, int axis, uint32_t token) {
+    float half_turns;
     if (p.positions) {
-        at = (double)__ldg(p.positions + 3 * (int64_t)token + a);
+        const double turns = (double)__ldg(p.positions + 3 * (int64_t)token + axis) * __longlong_as_double(r.origin);
+        half_turns = 2.0f * (float)(turns - rint(turns));
     } else {
         const uint32_t f = fdiv(token, p.plane), in = token - f * p.plane.d;
         const uint32_t row = fdiv(in, p.width), col = in - row * p.width.d;
-        at = fma(p.step[a], (double)(a == 0 ? f : a == 1 ? row : col), p.origin[a]);
+        const uint64_t at = (uint64_t)r.origin + (uint64_t)r.step * (axis == 0 ? f : axis == 1 ? row : col);
+        half_turns = (float)(int64_t)at * 0x1p-63f;
     }
-    // the angle in turns, its whole turns dropped in fp64: what is left keeps fp32's relative precision
-    const double turns = at * p.turns[i];
     float s, c;
-    sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+    sincospif(half_turns, &s, &c);
     return make_float2(c, p.inverse ? -s : s);
-}
-
-// The table of a CTA's tokens.
-__device__ __forceinline__ void rope_table(const RopeParams &p, uint32_t token0, uint32_t n, float2 *table) {
-    for (uint32_t e = threadIdx.x; e < n * p.all_pairs; e += kRopeThreads) {
-        const uint32_t tok = e / (uint32_t)p.all_pairs, i = e - tok * p.all_pairs;
-        if (i < (uint32_t)p.pairs) table[e] = rope_angle(p, token0 + tok, i);   // others are never read
-    }
 }
 
 __device__ __forceinline__ void turn(float &a, float &b, const float2 &cs) {
@@ -159,66 +141,99 @@ __device__ __forceinline__ void turn(float &a, float &b, const float2 &cs) {
     b = fmaf(x, cs.y, y * cs.x);
 }
 
-template <typename T, int FORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int V = Chunk<T>::V, U = kRopeUnroll;
+// NS items of a token per thread: one while a token has no more items than the CTA threads (then `abreast` tokens side
+// by side), else two, 256 apart, of the 512 that blockIdx.y names.
+template <typename T, int FORM, int NS>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int V = Chunk<T>::V, U = 4 / NS;          // tokens in flight
     __shared__ __align__(16) float2 table[kRopeTable];
-    const uint32_t token0 = blockIdx.x * p.tokens_per_cta;
-    const uint32_t n = min(p.tokens_per_cta, p.tokens - token0);
-    const uint32_t items = n * p.items.d;
-    for (uint32_t base = 0; base < items; base += p.batch) {
-        const uint32_t end = min(items, base + p.batch);
-        RopeItem item[U];
-        uint4 v0[U], v1[FORM == kRopeTwoChunks ? U : 1];
-        uint32_t apart[U];
+    __shared__ RopePair pairs[kRopeMaxPairs];
+    for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) pairs[i] = p.pair[i];
+
+    const uint32_t token0 = blockIdx.x * p.tokens_per_cta, n = min(p.tokens_per_cta, p.tokens - token0);
+    const uint32_t side = NS == 1 ? fdiv(threadIdx.x, p.items) : 0;
+    const char *x[NS];
+    char *y[NS];
+    int64_t x_step[NS], y_step[NS];
+    uint32_t apart[NS];                        // bytes to an item's second chunk
+    int pair0[NS];                             // its first pair
+    bool live[NS];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t it = base + u * kRopeThreads + threadIdx.x;
-            if (it >= end) continue;
-            item[u] = rope_item(p, it, token0);
-            if constexpr (FORM == kRopeTwoChunks) {
-                uint32_t c;
-                rope_two<T>(p, item[u].j, c, apart[u]);
-                item[u].x += c * sizeof(T);
-                item[u].y += c * sizeof(T);
-                v1[u] = *reinterpret_cast<const uint4 *>(item[u].x + apart[u] * sizeof(T));
-            } else {
-                item[u].x += item[u].j * 16;
-                item[u].y += item[u].j * 16;
+    for (int s = 0; s < NS; ++s) {
+        const uint32_t it = NS == 1 ? threadIdx.x - side * p.items.d : blockIdx.y * 512 + s * 256 + threadIdx.x;
+        live[s] = NS == 1 ? side < p.abreast : it < p.items.d;
+        int k = 0;
+#pragma unroll
+        for (int i = 1; i < NOMAS_ROPE_MAX_TENSORS; ++i)
+            if (i < p.n_tensors && it >= p.t[i].first_item) k = i;
+        const RopeTensor &t = p.t[k];
+        const uint32_t in = it - t.first_item, head = fdiv(in, p.per_head), j = in - head * p.per_head.d;
+        uint32_t c = j * V, gap = 0;
+        if constexpr (FORM == kRopeTwoChunks) rope_two<T>(p, j, c, gap);
+        apart[s] = gap * sizeof(T);
+        pair0[s] = j * (FORM == kRopeTwoChunks ? V : V / 2);
+        const int64_t tok = (int64_t)token0 + side;
+        x[s] = t.x + tok * t.x_tok + (int64_t)head * t.x_head + c * sizeof(T);
+        y[s] = t.y + tok * t.y_tok + (int64_t)head * t.y_head + c * sizeof(T);
+        x_step[s] = t.x_tok * p.abreast;
+        y_step[s] = t.y_tok * p.abreast;
+    }
+    for (uint32_t at = 0; at < n; at += U * p.abreast) {
+        uint4 v0[U][NS], v1[FORM == kRopeTwoChunks ? U : 1][NS];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                if (live[s] && at + u * p.abreast + side < n) {
+                    v0[u][s] = *reinterpret_cast<const uint4 *>(x[s]);
+                    if constexpr (FORM == kRopeTwoChunks) v1[u][s] = *reinterpret_cast<const uint4 *>(x[s] + apart[s]);
+                }
+                x[s] += x_step[s];
             }
-            v0[u] = *reinterpret_cast<const uint4 *>(item[u].x);
-        }
-        if (base == 0) {
-            rope_table(p, token0, n, table);
+        if (at == 0) {
+            __syncthreads();                   // the pairs
+            for (uint32_t e = threadIdx.x; e < n * p.all_pairs; e += blockDim.x) {
+                const uint32_t tok = fdiv(e, p.per_token), i = e - tok * p.all_pairs;
+                if (i < (uint32_t)p.pairs) table[e] = rope_angle(p, pairs[i], rope_axis(p, i), token0 + tok);
+            }
             __syncthreads();
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t it = base + u * kRopeThreads + threadIdx.x;
-            if (it >= end) continue;
-            const float2 *cs = table + item[u].token * p.all_pairs;
-            float a[V];
-            unpack(v0[u], a);
-            if constexpr (FORM == kRopeInside) {
-                const int i0 = item[u].j * (V / 2);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < V / 2; ++i)
-                    if (i0 + i < p.pairs) turn(a[2 * i], a[2 * i + 1], cs[i0 + i]);
-                *reinterpret_cast<uint4 *>(item[u].y) = keep_behind<V>(pack(a), v0[u], 2 * (p.pairs - i0));
-            } else {
-                const int i0 = item[u].j * V;
-                float b[V];
-                unpack(v1[u], b);
-                if (i0 < p.pairs) {            // whole items turn or pass
+            for (int s = 0; s < NS; ++s) {
+                const uint32_t tok = at + u * p.abreast + side;
+                if (live[s] && tok < n) {
+                    const float2 *cs = table + tok * p.all_pairs + pair0[s];
+                    float a[V];
+                    unpack(v0[u][s], a);
+                    if constexpr (FORM == kRopeInside) {
+                        if (pair0[s] + V / 2 <= p.pairs) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) turn(a[i], b[i], cs[i0 + i]);
-                    v0[u] = pack(a);
-                    v1[u] = pack(b);
+                            for (int i = 0; i < V / 2; ++i) turn(a[2 * i], a[2 * i + 1], cs[i]);
+                            v0[u][s] = pack(a);
+                        } else {               // the axes end in this chunk, or before it
+#pragma unroll
+                            for (int i = 0; i < V / 2; ++i)
+                                if (pair0[s] + i < p.pairs) turn(a[2 * i], a[2 * i + 1], cs[i]);
+                            v0[u][s] = keep_behind<V>(pack(a), v0[u][s], 2 * (p.pairs - pair0[s]));
+                        }
+                        *reinterpret_cast<uint4 *>(y[s]) = v0[u][s];
+                    } else {
+                        if (pair0[s] < p.pairs) {      // whole items turn or pass
+                            float b[V];
+                            unpack(v1[u][s], b);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) turn(a[i], b[i], cs[i]);
+                            v0[u][s] = pack(a);
+                            v1[u][s] = pack(b);
+                        }
+                        *reinterpret_cast<uint4 *>(y[s]) = v0[u][s];
+                        *reinterpret_cast<uint4 *>(y[s] + apart[s]) = v1[u][s];
+                    }
                 }
-                *reinterpret_cast<uint4 *>(item[u].y) = v0[u];
-                *reinterpret_cast<uint4 *>(item[u].y + apart[u] * sizeof(T)) = v1[u];
+                y[s] += y_step[s];
             }
-        }
     }
 }
 
@@ -237,18 +252,15 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { retur
 template <typename T, int NP>
 __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const __grid_constant__ RopeParams p) {
     constexpr int U = NP <= 2 ? 4 : 2;         // rows in flight
-    const uint32_t item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t token = fdiv(item, p.items), part = item - token * p.items.d;
-    if (token >= p.tokens) return;
+    const uint32_t lane = threadIdx.x & 31;
     uint32_t c1[NP], c2[NP];
-    float2 cs[NP];
+    RopePair pair[NP];
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
         const int i = lane + 32 * k;
         c1[k] = 2 * i, c2[k] = 2 * i + 1;
-        cs[k] = make_float2(1.0f, 0.0f);
         if (i >= p.pairs) continue;
-        cs[k] = rope_angle(p, token, i);
+        pair[k] = p.pair[i];
 #pragma unroll
         for (int a = 0; a < 3; ++a) {
             const int s = p.axis_at[a], e = p.axis_at[a + 1];
@@ -258,36 +270,46 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const __grid_c
             }
         }
     }
-    const uint32_t first = part * p.batch, last = min(first + p.batch, p.all_rows);
-    for (uint32_t r0 = first; r0 < last; r0 += U) {
-        T a[U][NP], b[U][NP];
-        T *to[U];
+    for (uint32_t item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); item < p.warp_items;
+         item += gridDim.x * (kRopeThreads / 32)) {
+        const uint32_t token = fdiv(item, p.items), part = item - token * p.items.d;
+        float2 cs[NP];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t row = min(r0 + u, last - 1);
-            int t = 0;
-#pragma unroll
-            for (int i = 1; i < NOMAS_ROPE_MAX_TENSORS; ++i)
-                if (i < p.n_tensors && row >= p.t[i].first_row) t = i;
-            const uint32_t head = row - p.t[t].first_row;
-            const T *x = reinterpret_cast<const T *>(p.t[t].x + token * p.t[t].x_tok + head * p.t[t].x_head);
-            to[u] = reinterpret_cast<T *>(p.t[t].y + token * p.t[t].y_tok + head * p.t[t].y_head);
-#pragma unroll
-            for (int k = 0; k < NP; ++k)
-                if ((int)lane + 32 * k < p.all_pairs) a[u][k] = x[c1[k]], b[u][k] = x[c2[k]];
+        for (int k = 0; k < NP; ++k) {
+            const int i = lane + 32 * k;
+            if (i < p.pairs) cs[k] = rope_angle(p, pair[k], rope_axis(p, i), token);
         }
+        const uint32_t first = part * p.rows_per_warp, last = min(first + p.rows_per_warp, p.all_rows);
+        for (uint32_t r0 = first; r0 < last; r0 += U) {
+            T a[U][NP], b[U][NP];
+            T *to[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (r0 + u >= last) break;
+            for (int u = 0; u < U; ++u) {
+                const uint32_t row = min(r0 + u, last - 1);
+                int t = 0;
 #pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                if ((int)lane + 32 * k >= p.all_pairs) continue;
-                if ((int)lane + 32 * k < p.pairs) {
-                    float v = value_of(a[u][k]), w = value_of(b[u][k]);
-                    turn(v, w, cs[k]);
-                    a[u][k] = rounded<T>(v), b[u][k] = rounded<T>(w);
+                for (int i = 1; i < NOMAS_ROPE_MAX_TENSORS; ++i)
+                    if (i < p.n_tensors && row >= p.t[i].first_row) t = i;
+                const uint32_t head = row - p.t[t].first_row;
+                const T *x = reinterpret_cast<const T *>(p.t[t].x + token * p.t[t].x_tok + head * p.t[t].x_head);
+                to[u] = reinterpret_cast<T *>(p.t[t].y + token * p.t[t].y_tok + head * p.t[t].y_head);
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    if ((int)lane + 32 * k < p.all_pairs) a[u][k] = x[c1[k]], b[u][k] = x[c2[k]];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r0 + u >= last) break;
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    if ((int)lane + 32 * k >= p.all_pairs) continue;
+                    if ((int)lane + 32 * k < p.pairs) {
+                        float v = value_of(a[u][k]), w = value_of(b[u][k]);
+                        turn(v, w, cs[k]);
+                        a[u][k] = rounded<T>(v), b[u][k] = rounded<T>(w);
+                    }
+                    to[u][c1[k]] = a[u][k], to[u][c2[k]] = b[u][k];
                 }
-                to[u][c1[k]] = a[u][k], to[u][c2[k]] = b[u][k];
             }
         }
     }
@@ -305,12 +327,22 @@ static int launch_rope_pairs(unsigned grid, const RopeParams &p, cudaStream_t st
 }
 
 template <typename T>
-static int launch_rope(RopeForm form, unsigned grid, const RopeParams &p, cudaStream_t st) {
-    if (form == kRopeInside)
-        rope_kernel<T, kRopeInside><<<grid, kRopeThreads, 0, st>>>(p);
-    else
-        rope_kernel<T, kRopeTwoChunks><<<grid, kRopeThreads, 0, st>>>(p);
+static int launch_rope(RopeForm form, dim3 grid, unsigned threads, const RopeParams &p, cudaStream_t st) {
+    const bool two = p.items.d > kRopeThreads;
+    if (form == kRopeInside) {
+        if (two) rope_kernel<T, kRopeInside, 2><<<grid, threads, 0, st>>>(p);
+        else rope_kernel<T, kRopeInside, 1><<<grid, threads, 0, st>>>(p);
+    } else {
+        if (two) rope_kernel<T, kRopeTwoChunks, 2><<<grid, threads, 0, st>>>(p);
+        else rope_kernel<T, kRopeTwoChunks, 1><<<grid, threads, 0, st>>>(p);
+    }
     return check_launch("rope_kernel launch");
+}
+
+// The fraction of a number of turns, in 2^-64.
+static int64_t rope_fraction(double turns) {
+    const double part = turns - std::nearbyint(turns);                 // exact, -1/2 .. 1/2
+    return (int64_t)((uint64_t)std::llrint(part * 0x1p62) << 2);
 }
 
 static bool rope_spec_ok(const nomas_rope_spec *s) {
@@ -340,11 +372,8 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
     if (grid) {
         if (grid->grid_h < 1 || grid->grid_w < 1 || (int64_t)grid->grid_h * grid->grid_w >= (int64_t)1 << 31)
             return NOMAS_EINVAL;
-        for (int a = 0; a < 3; ++a) {
+        for (int a = 0; a < 3; ++a)
             if (!std::isfinite(grid->origin[a]) || !std::isfinite(grid->step[a])) return NOMAS_EINVAL;
-            p.origin[a] = grid->origin[a];
-            p.step[a] = grid->step[a];
-        }
         p.plane = make_fastdiv((uint32_t)(grid->grid_h * grid->grid_w));
         p.width = make_fastdiv((uint32_t)grid->grid_w);
     } else if (reinterpret_cast<uintptr_t>(positions) % 4 != 0) {
@@ -378,7 +407,7 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
                             t.x_head_stride * esize, t.y_tok_stride * esize, t.y_head_stride * esize, (uint32_t)items, p.all_rows};
         p.all_rows += (uint32_t)t.heads;
         items += t.heads * per_head;
-        if (items >= (int64_t)1 << 24) return NOMAS_EUNSUPPORTED;
+        if (items >= (int64_t)1 << 24) return NOMAS_EUNSUPPORTED;      // 512 a CTA along a grid's y
     }
     if (tokens == 0) return NOMAS_OK;
     // theta^(-2 i / d) as powers of one root: 128 products in the 64-bit mantissa of long double stay exact to fp64
@@ -387,37 +416,51 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
         if (spec->axis_dim[a] == 0) continue;
         const long double root = std::pow((long double)spec->theta, -2.0L / spec->axis_dim[a]);
         long double at = 1.0L / 6.283185307179586476925286766559L;
-        for (int i = 0; i < spec->axis_dim[a] / 2; ++i, at *= root) p.turns[pair++] = (double)at;
+        for (int i = 0; i < spec->axis_dim[a] / 2; ++i, ++pair, at *= root) {
+            const double turns = (double)at;
+            if (grid)
+                p.pair[pair] = RopePair{rope_fraction(turns * grid->origin[a]), rope_fraction(turns * grid->step[a])};
+            else
+                std::memcpy(&p.pair[pair].origin, &turns, sizeof(turns));
+        }
     }
     p.positions = positions;
     p.items = make_fastdiv((uint32_t)items);
     p.per_head = make_fastdiv((uint32_t)per_head);
+    p.per_token = make_fastdiv((uint32_t)p.all_pairs);
     p.tokens = (uint32_t)tokens;
     p.n_tensors = n_tensors;
     p.inverse = inverse != 0;
-    // a CTA takes as many tokens as fill one round of loads, as far as their table fits and every SM still
-    // gets a CTA
-    const int64_t round = (int64_t)kRopeUnroll * kRopeThreads;
-    int64_t per_cta = round / items;
-    const int64_t spread = (tokens + sm_count() - 1) / sm_count();
-    if (per_cta > kRopeTable / p.all_pairs) per_cta = kRopeTable / p.all_pairs;
-    if (per_cta > spread) per_cta = spread;
-    if (per_cta < 1) per_cta = 1;
-    p.tokens_per_cta = (uint32_t)per_cta;
-    p.batch = (uint32_t)round;
     DeviceScope dev(tensors[0].x);
     if (dev.rc) return dev.rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t sms = sm_count();
     if (form == kRopePairs) {
         // rows that share a token's angles: 32, fewer while there would be fewer than 16 warps an SM
-        p.batch = 32;
-        while (p.batch > 4 && tokens * ((p.all_rows + p.batch - 1) / p.batch) < (int64_t)16 * sm_count()) p.batch /= 2;
-        const int64_t parts = (p.all_rows + p.batch - 1) / p.batch, warps = tokens * parts;
+        p.rows_per_warp = 32;
+        while (p.rows_per_warp > 4 && tokens * ((p.all_rows + p.rows_per_warp - 1) / p.rows_per_warp) < 16 * sms)
+            p.rows_per_warp /= 2;
+        const int64_t parts = (p.all_rows + p.rows_per_warp - 1) / p.rows_per_warp, warps = tokens * parts;
         if (warps >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
         p.items = make_fastdiv((uint32_t)parts);
-        const unsigned grid = (unsigned)((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
-        return dtype == NOMAS_DTYPE_BF16 ? launch_rope_pairs<__nv_bfloat16>(grid, p, st) : launch_rope_pairs<float>(grid, p, st);
+        p.warp_items = (uint32_t)warps;
+        int64_t grid = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+        if (grid > 4 * sms) grid = 4 * sms;    // as many as run at once: a warp sets its pairs up once
+        return dtype == NOMAS_DTYPE_BF16 ? launch_rope_pairs<__nv_bfloat16>((unsigned)grid, p, st)
+                                         : launch_rope_pairs<float>((unsigned)grid, p, st);
     }
-    const unsigned ctas = (unsigned)((tokens + per_cta - 1) / per_cta);
-    return dtype == NOMAS_DTYPE_BF16 ? launch_rope<__nv_bfloat16>(form, ctas, p, st) : launch_rope<float>(form, ctas, p, st);
+    // threads for `abreast` tokens side by side; a CTA takes two rounds of loads of them, fewer while every SM
+    // would not get four CTAs, at most a table
+    p.abreast = items > kRopeThreads ? 1 : (uint32_t)(kRopeThreads / items);
+    if (p.abreast > tokens) p.abreast = (uint32_t)tokens;
+    const unsigned threads = items > kRopeThreads ? kRopeThreads : (unsigned)((p.abreast * items + 31) / 32 * 32);
+    const int64_t parts = items > kRopeThreads ? (items + 511) / 512 : 1;
+    int64_t per_cta = 2 * (items > kRopeThreads ? 2 : 4) * p.abreast;
+    if (per_cta > tokens * parts / (4 * sms)) per_cta = tokens * parts / (4 * sms);
+    if (per_cta > kRopeTable / p.all_pairs) per_cta = kRopeTable / p.all_pairs;
+    if (per_cta < p.abreast) per_cta = p.abreast <= kRopeTable / p.all_pairs ? p.abreast : kRopeTable / p.all_pairs;
+    p.tokens_per_cta = (uint32_t)per_cta;
+    const dim3 grid_dim((unsigned)((tokens + per_cta - 1) / per_cta), (unsigned)parts);
+    return dtype == NOMAS_DTYPE_BF16 ? launch_rope<__nv_bfloat16>(form, grid_dim, threads, p, st)
+                                     : launch_rope<float>(form, grid_dim, threads, p, st);
 }
