@@ -400,11 +400,14 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(cons
     ring_wait<0>();
 }
 
+// Floats of a row of dw or db in the workspace: a multiple of 16 bytes.
+__host__ __device__ constexpr int64_t part_pitch(int64_t cols) { return (cols + 3) / 4 * 4; }
+
 struct NormBwdParams {
     const void *dy, *x, *w;
     const float *mean, *rstd;
     void *dx;
-    float *dw, *db, *part;      // part: [CTAs][2][2][cols] (share, head or tail of it, dw or db)
+    float *dw, *db, *part;      // part: [CTAs][2][2][part_pitch] (share, head or tail of it, dw or db)
     int64_t lddy, ldx, lddx, ldp, ldg;
     uint32_t rows, cols, share; // share: rows of a CTA
     int32_t by_group;           // layernorm_grad_kernel: a grid row is a group
@@ -478,7 +481,7 @@ struct BwdRing {
 };
 
 template <typename TX, typename TY, int CH, int NV, int R, int T>
-__global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(T, T == 256 || (CH == 1 && NV == 8) ? 2 : 1) layernorm_bwd_kernel(const NormBwdParams p) {
     constexpr bool RING = BwdRing<TX, TY, CH, NV, R, T>::kStages > 0;
     constexpr int S = RING ? BwdRing<TX, TY, CH, NV, R, T>::kStages : 1, XB = CH * sizeof(TX), YB = CH * sizeof(TY);
     extern __shared__ __align__(16) uint8_t smem[];
@@ -522,10 +525,36 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwd
         }
         ring_commit();
     };
+    // without a ring the next batch waits in registers
+    TX next_x[RING ? 1 : R][RING ? 1 : E];
+    TY next_y[RING ? 1 : R][RING ? 1 : E];
+    auto fetch_registers = [&]() {
+        if (fetch_row >= end) return;
+        if (fetch_row >= fetch_stop)
+            fetch_stop = (uint32_t)min((int64_t)end, ((int64_t)fdiv(fetch_row, p.group) + 1) * p.group.d);
+        const TX *x = from_x + fetch_row * p.ldx;
+        const TY *dy = from_y + fetch_row * p.lddy;
+#pragma unroll
+        for (int r = 0; r < (RING ? 0 : R); ++r, x += step_x, dy += step_y) {
+            const bool live = fetch_row + r * teams + mine < fetch_stop;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const bool in = live && (uint32_t)(lane + j * team) * CH < p.cols;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    next_x[r][j * CH + i] = in ? x[j * team * CH + i] : (TX)0.0f;
+                    next_y[r][j * CH + i] = in ? dy[j * team * CH + i] : (TY)0.0f;
+                }
+            }
+        }
+        fetch_row = min(fetch_row + R * teams, fetch_stop);
+    };
     int stage = 0, last = S - 1;
     if constexpr (RING) {
 #pragma unroll
         for (int k = 0; k < S - 1; ++k) fetch(k);
+    } else {
+        fetch_registers();
     }
     for (uint32_t row = begin; row < end;) {
         const uint32_t g = fdiv(row, p.group);
@@ -560,23 +589,19 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwd
             }
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const uint32_t at = r0 + r * teams + mine;
-                const bool live = at < stop;
-                const TX *x = static_cast<const TX *>(p.x) + (int64_t)at * p.ldx;
-                const TY *dy = static_cast<const TY *>(p.dy) + (int64_t)at * p.lddy;
                 float fx[NV][CH], fy[NV][CH];
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const uint32_t c = (uint32_t)(lane + j * team) * CH;
-#pragma unroll
-                    for (int i = 0; i < CH; ++i) fx[j][i] = fy[j][i] = 0.0f;
                     if constexpr (RING) {
                         const int slot = (stage * R + r) * NV + j;
                         load_chunk<CH>(reinterpret_cast<const TX *>(ring_x + slot * T * XB), fx[j]);
                         load_chunk<CH>(reinterpret_cast<const TY *>(ring_y + slot * T * YB), fy[j]);
-                    } else if (live && c < p.cols) {
-                        load_chunk<CH>(x + c, fx[j]);
-                        load_chunk<CH>(dy + c, fy[j]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            fx[j][i] = (float)next_x[r][j * CH + i];
+                            fy[j][i] = (float)next_y[r][j * CH + i];
+                        }
                     }
                 }
 #pragma unroll
@@ -585,6 +610,7 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwd
                     gy[r][k] = pair_of(fy[2 * k / CH][2 * k % CH], fy[(2 * k + 1) / CH][(2 * k + 1) % CH]);
                 }
             }
+            if constexpr (!RING) fetch_registers();
             last = stage;
             stage = stage + 1 == S ? 0 : stage + 1;
             // columns past the row and rows past the group have dy = 0: what their xhat is adds nothing
@@ -632,8 +658,8 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwd
                 db = p.db ? p.db + (int64_t)g * p.ldg : nullptr;
                 wide = p.grad_wide;
             } else {            // slot 0: the group began in an earlier share, 1: it goes on in a later one
-                dw = p.part + ((int64_t)blockIdx.x * 2 + (g0 < begin ? 0 : 1)) * 2 * p.cols;
-                db = dw + p.cols;
+                dw = p.part + ((int64_t)blockIdx.x * 2 + (g0 < begin ? 0 : 1)) * 2 * part_pitch(p.cols);
+                db = dw + part_pitch(p.cols);
             }
             flush_grads<CH, NV, T>(p, aw, ab, dw, db, wide, meet);
         }
@@ -643,32 +669,44 @@ __global__ void __launch_bounds__(T, 512 / T) layernorm_bwd_kernel(const NormBwd
 }
 
 // Groups that several shares hold.  Row y of the grid is group y, or with more groups than shares the group
-// that begins in share y and goes on behind it, if there is one.  32 columns of dw or of db a CTA, kGradRows
-// shares at a time.
-constexpr int kGradRows = 8;
-
-__global__ void __launch_bounds__(32 * kGradRows) layernorm_grad_kernel(const NormBwdParams p) {
-    __shared__ float red[kGradRows][33];
+// that begins in share y and goes on behind it, if there is one.  128 columns of dw or of db a CTA, ROWS shares
+// at a time.
+template <int ROWS>
+__global__ void __launch_bounds__(32 * ROWS) layernorm_grad_kernel(const NormBwdParams p) {
+    __shared__ float4 red[ROWS][32];
     griddep_wait();
     const int64_t g = p.by_group ? blockIdx.y : fdiv((uint32_t)min((int64_t)p.rows, ((int64_t)blockIdx.y + 1) * p.share) - 1, p.group);
     const int64_t g0 = g * p.group.d, g1 = min(g0 + (int64_t)p.group.d, (int64_t)p.rows);
-    const int64_t first = g0 / p.share, final = (g1 - 1) / p.share;
+    const int64_t first = g0 / p.share, final = (g1 - 1) / p.share, pitch = part_pitch(p.cols);
     if (first == final || (!p.by_group && first != blockIdx.y)) return;
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t at = (int64_t)blockIdx.x * 32 + lane;         // 0 .. 2 cols - 1: dw then db
-    float s = 0.0f;
-    if (at < 2 * (int64_t)p.cols) {
+    const int64_t at = (int64_t)blockIdx.x * 128 + lane * 4;            // 0 .. 2 pitch - 1: dw then db
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (at < 2 * pitch) {
         const float *part = p.part + at;
 #pragma unroll 4
-        for (int64_t b = first + k; b <= final; b += kGradRows) s += part[(b * 2 + (b == first ? 1 : 0)) * 2 * p.cols];
+        for (int64_t b = first + k; b <= final; b += ROWS) {
+            const float4 v = *reinterpret_cast<const float4 *>(part + (b * 2 + (b == first ? 1 : 0)) * 2 * pitch);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
     }
     red[k][lane] = s;
     __syncthreads();
-    if (k != 0 || at >= 2 * (int64_t)p.cols) return;
+    if (k != 0 || at >= 2 * pitch) return;
 #pragma unroll
-    for (int i = 1; i < kGradRows; ++i) s += red[i][lane];
-    float *out = at < p.cols ? p.dw : p.db;
-    if (out) out[g * p.ldg + (at < p.cols ? at : at - p.cols)] = s;
+    for (int i = 1; i < ROWS; ++i) {
+        const float4 v = red[i][lane];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const int64_t col = at < pitch ? at : at - pitch;
+    float *out = at < pitch ? p.dw : p.db;
+    if (!out) return;
+    out += g * p.ldg + col;
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    if (p.grad_wide && col + 4 <= p.cols)
+        store_chunk<4>(out, v);
+    else
+        for (int i = 0; i < 4 && col + i < p.cols; ++i) out[i] = v[i];
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -807,21 +845,32 @@ static int launch_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     if (rc || ctas == 1 || (!p.dw && !p.db)) return rc;
     const int64_t groups = ((int64_t)p.rows + p.group.d - 1) / p.group.d;
     p.by_group = groups < ctas;
-    const dim3 grid((unsigned)((2 * (int64_t)p.cols + 31) / 32), (unsigned)(p.by_group ? groups : ctas - 1));
-    const cudaError_t e = launch_pdl(layernorm_grad_kernel, grid, dim3(32 * kGradRows), 0, st, p);
+    const dim3 grid((unsigned)((2 * part_pitch(p.cols) + 127) / 128), (unsigned)(p.by_group ? groups : ctas - 1));
+    // a group's shares: as many rows of threads as give each a few to add
+    const int64_t shares = p.group.d / p.share + 2 < ctas ? p.group.d / p.share + 2 : ctas;
+    const bool many = shares > 64;
+    const cudaError_t e = launch_pdl(many ? layernorm_grad_kernel<32> : layernorm_grad_kernel<8>, grid,
+                                     dim3(many ? 1024 : 256), 0, st, p);
     return e == cudaSuccess ? NOMAS_OK : cuda_fail("layernorm_grad_kernel launch", (int)e, cudaGetErrorString(e));
 }
 
-// Values of a row per thread: 8 with 4 rows at a time, 16 with 2, then teams of 512 threads.
+// Values of a row per thread: 8 with 4 rows at a time, 16 with 2, then teams of 512 threads.  Narrow layouts hold the
+// next rows in registers and take half as many values.
 template <typename TX, typename TY, int CH>
 static int pick_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
     constexpr int kLeast = CH == 1 ? 2 : 1;     // pairs of values
     p.team_log2 = team_of(chunks, kLeast, 8);
     if (chunks <= kLeast * 256) return launch_bwd<TX, TY, CH, kLeast, 4, 256>(p, ctas, st);
-    if (p.cols <= 2048) return launch_bwd<TX, TY, CH, 8 / CH, CH == 1 ? 2 : 4, 256>(p, ctas, st);
-    if (p.cols <= 4096) return launch_bwd<TX, TY, CH, 16 / CH, CH == 1 ? 1 : 2, 256>(p, ctas, st);
-    p.team_log2 = 9;
+    if constexpr (CH == 1) {
+        if (p.cols <= 2048) return launch_bwd<TX, TY, 1, 8, 1, 256>(p, ctas, st);
+        p.team_log2 = 9;
+        if (p.cols <= 4096) return launch_bwd<TX, TY, 1, 8, 1, 512>(p, ctas, st);
+    } else {
+        if (p.cols <= 2048) return launch_bwd<TX, TY, CH, 8 / CH, 4, 256>(p, ctas, st);
+        if (p.cols <= 4096) return launch_bwd<TX, TY, CH, 16 / CH, 2, 256>(p, ctas, st);
+        p.team_log2 = 9;
+    }
     if (p.cols <= 8192) return launch_bwd<TX, TY, CH, 16 / CH, 1, 512>(p, ctas, st);
     return launch_bwd<TX, TY, CH, 32 / CH, 1, 512>(p, ctas, st);
 }
@@ -871,7 +920,7 @@ extern "C" size_t nomas_layernorm_workspace_bytes(int64_t rows, int64_t cols, in
     if (check_norm(rows, cols, rows_per_group)) return 0;
     int64_t share, ctas;
     bwd_shares(rows, cols, &share, &ctas);
-    const size_t n = ctas > 1 ? (size_t)ctas * 4 * (size_t)cols * sizeof(float) : 0;
+    const size_t n = ctas > 1 ? (size_t)ctas * 4 * (size_t)part_pitch(cols) * sizeof(float) : 0;
     return n < 16 ? 16 : n;
 }
 
