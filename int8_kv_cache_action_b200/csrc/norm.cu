@@ -147,6 +147,11 @@ __device__ __forceinline__ void store_pairs(T *p, const Pair (&v)[CH / 2]) {
     store_chunk<CH>(p, f);
 }
 
+template <int V>
+constexpr int LOG2 = V <= 1 ? 0 : 1 + LOG2<V / 2>;
+template <>
+constexpr int LOG2<1> = 0;
+
 // Sums of N values (N = 1, 2, 4, 8) over a team of 2^log2 threads; every thread gets them, in an order that
 // depends on the team alone.  In a warp the N values are halved between the lanes as they are added up (N - 1
 // + log2(32 / N) shuffles, not 5 N).  Teams of more than a warp meet in `red` (N floats per warp of the CTA and
@@ -283,13 +288,15 @@ struct FwdRing {
     static constexpr int kBytes = kStages * kStage;
 };
 
-template <typename TX, typename TY, int CH, int NV, int R, int T>
+// ALONE: one team a CTA (rows of more than half of what its threads hold at a chunk each).
+template <typename TX, typename TY, int CH, int NV, int R, int T, bool ALONE>
 __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(const NormParams p) {
     constexpr int S = FwdRing<TX, CH, NV, R, T>::kStages, BYTES = CH * sizeof(TX), P = CH / 2;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2 * (T / 32) * R];
-    const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), mine = threadIdx.x >> p.team_log2;
-    const uint32_t teams = T >> p.team_log2;
+    const int team_log2 = ALONE ? LOG2<T> : p.team_log2, team = 1 << team_log2;
+    const int lane = threadIdx.x & (team - 1), mine = ALONE ? 0 : threadIdx.x >> team_log2;
+    const uint32_t teams = T >> team_log2;
     const uint32_t begin = blockIdx.x * p.share, end = min(p.rows, begin + p.share);
     const uint8_t *ring = smem + threadIdx.x * BYTES;
     const float inv = 1.0f / (float)p.cols;
@@ -356,7 +363,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(cons
             }
             last = stage;
             stage = stage + 1 == S ? 0 : stage + 1;
-            team_sum<R>(s, p.team_log2, red, parity);
+            team_sum<R>(s, team_log2, red, parity);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 mean[r] = s[r] * inv;
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(cons
                 }
                 s[r] = pair_sum(sum);
             }
-            team_sum<R>(s, p.team_log2, red, parity);
+            team_sum<R>(s, team_log2, red, parity);
             TY *y = static_cast<TY *>(p.y) + (int64_t)(r0 + mine) * p.ldy + lane * CH;
             const int64_t out_step = (int64_t)teams * p.ldy;
 #pragma unroll
@@ -416,14 +423,10 @@ struct NormBwdParams {
     float unit;
 };
 
-// Whether several teams of a CTA can share columns: a thread with more values has a team as large as the CTA.
-template <int CH, int NV>
-constexpr bool MEET = NV == 1 || (CH == 1 && NV == 2);
-
 // dw and db of a group (or of a part of one) from the CTA's threads: teams of the CTA hold the same columns.
-template <int CH, int NV, int T>
+template <int CH, int NV, int T, bool ALONE>
 __device__ __forceinline__ void flush_grads(const NormBwdParams &p, Pair (&sum_w)[NV * CH / 2], Pair (&sum_b)[NV * CH / 2],
-                                            float *dw, float *db, bool wide, float *meet) {
+                                            float *dw, float *db, bool wide, float *meet, int team_log2) {
     float aw[NV][CH], ab[NV][CH];
 #pragma unroll
     for (int k = 0; k < NV * CH / 2; ++k) {
@@ -431,9 +434,9 @@ __device__ __forceinline__ void flush_grads(const NormBwdParams &p, Pair (&sum_w
         pair_split(sum_b[k], ab[2 * k / CH][2 * k % CH], ab[(2 * k + 1) / CH][(2 * k + 1) % CH]);
         sum_w[k] = sum_b[k] = 0;
     }
-    const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), teams = T >> p.team_log2;
-    if (MEET<CH, NV> && teams > 1) {
-        const int stride = team * CH * NV, mine = threadIdx.x >> p.team_log2;
+    const int team = 1 << team_log2, lane = threadIdx.x & (team - 1), teams = T >> team_log2;
+    if constexpr (!ALONE) {
+        const int stride = team * CH * NV, mine = threadIdx.x >> team_log2;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             __syncthreads();
@@ -480,15 +483,16 @@ struct BwdRing {
     static constexpr int kBytes = kStages * kStage;
 };
 
-template <typename TX, typename TY, int CH, int NV, int R, int T>
+template <typename TX, typename TY, int CH, int NV, int R, int T, bool ALONE>
 __global__ void __launch_bounds__(T, T == 256 || (CH == 1 && NV == 8) ? 2 : 1) layernorm_bwd_kernel(const NormBwdParams p) {
     constexpr bool RING = BwdRing<TX, TY, CH, NV, R, T>::kStages > 0;
     constexpr int S = RING ? BwdRing<TX, TY, CH, NV, R, T>::kStages : 1, XB = CH * sizeof(TX), YB = CH * sizeof(TY);
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2 * (T / 32) * 2 * R];
-    __shared__ float meet[MEET<CH, NV> ? T * CH * NV : 1];
-    const int team = 1 << p.team_log2, lane = threadIdx.x & (team - 1), mine = threadIdx.x >> p.team_log2;
-    const uint32_t teams = T >> p.team_log2;
+    __shared__ float meet[ALONE ? 1 : T * CH * NV];
+    const int team_log2 = ALONE ? LOG2<T> : p.team_log2, team = 1 << team_log2;
+    const int lane = threadIdx.x & (team - 1), mine = ALONE ? 0 : threadIdx.x >> team_log2;
+    const uint32_t teams = T >> team_log2;
     const uint32_t begin = blockIdx.x * p.share, end = min(p.rows, begin + p.share);
     constexpr int E = NV * CH, P = E / 2;       // values of a row per thread, in pairs
     Pair aw[P], ab[P];
@@ -632,7 +636,7 @@ __global__ void __launch_bounds__(T, T == 256 || (CH == 1 && NV == 8) ? 2 : 1) l
                 s[2 * r + 1] = pair_sum(s2);
             }
             if (!p.dx) continue;
-            team_sum<2 * R>(s, p.team_log2, red, parity);
+            team_sum<2 * R>(s, team_log2, red, parity);
             TX *dx = static_cast<TX *>(p.dx) + (int64_t)(r0 + mine) * p.lddx + lane * CH;
             const int64_t out_step = (int64_t)teams * p.lddx;
 #pragma unroll
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(T, T == 256 || (CH == 1 && NV == 8) ? 2 : 1) l
                 dw = p.part + ((int64_t)blockIdx.x * 2 + (g0 < begin ? 0 : 1)) * 2 * part_pitch(p.cols);
                 db = dw + part_pitch(p.cols);
             }
-            flush_grads<CH, NV, T>(p, aw, ab, dw, db, wide, meet);
+            flush_grads<CH, NV, T, ALONE>(p, aw, ab, dw, db, wide, meet, team_log2);
         }
         row = stop;
     }
@@ -788,10 +792,10 @@ static int pick_row(NormParams &p, cudaStream_t st) {
     return launch_row<TX, TY, CH, CH == 1 ? 64 : 8>(p, st);
 }
 
-template <typename TX, typename TY, int CH, int NV, int R, int T>
+template <typename TX, typename TY, int CH, int NV, int R, int T, bool ALONE>
 static int launch_fwd(NormParams &p, cudaStream_t st) {
     constexpr int kBytes = FwdRing<TX, CH, NV, R, T>::kBytes;
-    auto kernel = layernorm_fwd_kernel<TX, TY, CH, NV, R, T>;
+    auto kernel = layernorm_fwd_kernel<TX, TY, CH, NV, R, T, ALONE>;
     static SmemAllowed allowed;
     const int rc = allowed(reinterpret_cast<const void *>(kernel), kBytes);
     if (rc) return rc;
@@ -808,12 +812,13 @@ template <typename TX, typename TY, int CH>
 static int pick_fwd(NormParams &p, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
     p.team_log2 = team_of(chunks, 1, 8);
-    if (chunks <= 256) return launch_fwd<TX, TY, CH, 1, 4, 256>(p, st);
-    if (p.cols <= 2048) return launch_fwd<TX, TY, CH, 8 / CH, 4, 256>(p, st);
-    if (p.cols <= 4096) return launch_fwd<TX, TY, CH, 16 / CH, 2, 256>(p, st);
+    if (chunks <= 128) return launch_fwd<TX, TY, CH, 1, 4, 256, false>(p, st);
+    if (chunks <= 256) return launch_fwd<TX, TY, CH, 1, 4, 256, true>(p, st);
+    if (p.cols <= 2048) return launch_fwd<TX, TY, CH, 8 / CH, 4, 256, true>(p, st);
+    if (p.cols <= 4096) return launch_fwd<TX, TY, CH, 16 / CH, 2, 256, true>(p, st);
     p.team_log2 = 9;
-    if (p.cols <= 8192) return launch_fwd<TX, TY, CH, 16 / CH, 2, 512>(p, st);
-    return launch_fwd<TX, TY, CH, 32 / CH, 1, 512>(p, st);
+    if (p.cols <= 8192) return launch_fwd<TX, TY, CH, 16 / CH, 2, 512, true>(p, st);
+    return launch_fwd<TX, TY, CH, 32 / CH, 1, 512, true>(p, st);
 }
 
 template <typename TX, typename TY>
@@ -833,10 +838,10 @@ static void bwd_shares(int64_t rows, int64_t cols, int64_t *share, int64_t *ctas
     *ctas = (rows + s - 1) / s;
 }
 
-template <typename TX, typename TY, int CH, int NV, int R, int T>
+template <typename TX, typename TY, int CH, int NV, int R, int T, bool ALONE>
 static int launch_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     constexpr int kBytes = BwdRing<TX, TY, CH, NV, R, T>::kBytes;
-    auto kernel = layernorm_bwd_kernel<TX, TY, CH, NV, R, T>;
+    auto kernel = layernorm_bwd_kernel<TX, TY, CH, NV, R, T, ALONE>;
     static SmemAllowed allowed;
     int rc = allowed(reinterpret_cast<const void *>(kernel), kBytes);
     if (rc) return rc;
@@ -861,18 +866,19 @@ static int pick_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
     constexpr int kLeast = CH == 1 ? 2 : 1;     // pairs of values
     p.team_log2 = team_of(chunks, kLeast, 8);
-    if (chunks <= kLeast * 256) return launch_bwd<TX, TY, CH, kLeast, 4, 256>(p, ctas, st);
+    if (chunks <= kLeast * 128) return launch_bwd<TX, TY, CH, kLeast, 4, 256, false>(p, ctas, st);
+    if (chunks <= kLeast * 256) return launch_bwd<TX, TY, CH, kLeast, 4, 256, true>(p, ctas, st);
     if constexpr (CH == 1) {
-        if (p.cols <= 2048) return launch_bwd<TX, TY, 1, 8, 1, 256>(p, ctas, st);
+        if (p.cols <= 2048) return launch_bwd<TX, TY, 1, 8, 1, 256, true>(p, ctas, st);
         p.team_log2 = 9;
-        if (p.cols <= 4096) return launch_bwd<TX, TY, 1, 8, 1, 512>(p, ctas, st);
+        if (p.cols <= 4096) return launch_bwd<TX, TY, 1, 8, 1, 512, true>(p, ctas, st);
     } else {
-        if (p.cols <= 2048) return launch_bwd<TX, TY, CH, 8 / CH, 4, 256>(p, ctas, st);
-        if (p.cols <= 4096) return launch_bwd<TX, TY, CH, 16 / CH, 2, 256>(p, ctas, st);
+        if (p.cols <= 2048) return launch_bwd<TX, TY, CH, 8 / CH, 4, 256, true>(p, ctas, st);
+        if (p.cols <= 4096) return launch_bwd<TX, TY, CH, 16 / CH, 2, 256, true>(p, ctas, st);
         p.team_log2 = 9;
     }
-    if (p.cols <= 8192) return launch_bwd<TX, TY, CH, 16 / CH, 1, 512>(p, ctas, st);
-    return launch_bwd<TX, TY, CH, 32 / CH, 1, 512>(p, ctas, st);
+    if (p.cols <= 8192) return launch_bwd<TX, TY, CH, 16 / CH, 1, 512, true>(p, ctas, st);
+    return launch_bwd<TX, TY, CH, 32 / CH, 1, 512, true>(p, ctas, st);
 }
 
 template <typename TX, typename TY>
