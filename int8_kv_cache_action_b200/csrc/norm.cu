@@ -5,11 +5,12 @@
 // x and writes dx, about 8 and 14 flops a value.  A row stays in the registers of a team of threads (a
 // power of two), so that the variance is a second sum over registers (exact differences, no sum of squares
 // that cancels) and memory is read once.
-//   layernorm_row_kernel   forward, one row per team, loads straight into registers: few rows (latency),
-//                          and layouts that allow no wide loads
+//   layernorm_row_kernel   forward, one row per team, loads straight into registers: few rows (latency), and
+//                          groups of few rows
 //   layernorm_fwd_kernel   forward, a CTA takes a contiguous share of the rows.  Every thread keeps its own
 //                          ring of 16-byte chunks in shared memory, filled by asynchronous copies several rows
-//                          ahead (nothing to synchronise: a thread reads what it copied).  A thread owns
+//                          ahead (nothing to synchronise: a thread reads what it copied); layouts that allow no
+//                          copies of 8 bytes hold the next rows in registers.  A thread owns
 //                          columns, whose weight and bias stay in its registers for a group, and takes R rows
 //                          at a time, which share the two exchanges of sums between the warps.
 //   layernorm_bwd_kernel   the same for dy and x; dw and db of a group add up in the registers in row order.  Groups inside a share are written at once; where a group
@@ -129,22 +130,6 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
     Pair r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
-}
-
-// CH consecutive values (4 or 8) at p as pairs, and back.
-template <int CH, typename T>
-__device__ __forceinline__ void load_pairs(const T *p, Pair (&v)[CH / 2]) {
-    float f[CH];
-    load_chunk<CH>(p, f);
-#pragma unroll
-    for (int i = 0; i < CH / 2; ++i) v[i] = pair_of(f[2 * i], f[2 * i + 1]);
-}
-template <int CH, typename T>
-__device__ __forceinline__ void store_pairs(T *p, const Pair (&v)[CH / 2]) {
-    float f[CH];
-#pragma unroll
-    for (int i = 0; i < CH / 2; ++i) pair_split(v[i], f[2 * i], f[2 * i + 1]);
-    store_chunk<CH>(p, f);
 }
 
 template <int V>
@@ -279,19 +264,22 @@ __global__ void __launch_bounds__(kNormThreads) layernorm_row_kernel(const NormP
     }
 }
 
-// Forward ring: stages of R rows of x, two to four, so that three CTAs of 256 threads (one of 512) fit an SM.
+// Forward ring: stages of R rows of x, two to four, so that three CTAs of 256 threads (one of 512) fit an SM; none in
+// narrow layouts (no copies of 8 bytes and more), where the next rows wait in registers.
 template <typename TX, int CH, int NV, int R, int T>
 struct FwdRing {
     static constexpr int kStage = R * NV * CH * (int)sizeof(TX) * T;
     static constexpr int kFit = (T == 256 ? 72 : 200) * 1024 / kStage;
-    static constexpr int kStages = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
+    static constexpr int kStages = CH == 1 ? 0 : kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
     static constexpr int kBytes = kStages * kStage;
 };
 
 // ALONE: one team a CTA (rows of more than half of what its threads hold at a chunk each).
 template <typename TX, typename TY, int CH, int NV, int R, int T, bool ALONE>
-__global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(const NormParams p) {
-    constexpr int S = FwdRing<TX, CH, NV, R, T>::kStages, BYTES = CH * sizeof(TX), P = CH / 2;
+__global__ void __launch_bounds__(T, T == 256 ? (CH == 1 ? 2 : 3) : 1) layernorm_fwd_kernel(const NormParams p) {
+    constexpr bool RING = CH > 1;
+    constexpr int S = RING ? FwdRing<TX, CH, NV, R, T>::kStages : 1, BYTES = CH * sizeof(TX);
+    constexpr int E = NV * CH, P = E / 2;       // values of a row per thread, in pairs
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float red[2 * (T / 32) * R];
     const int team_log2 = ALONE ? LOG2<T> : p.team_log2, team = 1 << team_log2;
@@ -306,6 +294,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(cons
     const uint32_t ring_at = smem_u32(ring);
     const TX *from = static_cast<const TX *>(p.x) + (int64_t)mine * p.ldx + lane * CH;
     const int64_t row_step = (int64_t)teams * p.ldx;
+    TX next[RING ? 1 : R][RING ? 1 : E];
     auto fetch = [&](int stage) {
         if (fetch_row < end) {
             if (fetch_row >= fetch_stop)
@@ -318,49 +307,68 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(cons
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const bool in = live && (uint32_t)(lane + j * team) * CH < p.cols;
-                    ring_load<BYTES>(to + (r * NV + j) * T * BYTES, in ? x + j * team * CH : p.x, in);
+                    if constexpr (RING)
+                        ring_load<BYTES>(to + (r * NV + j) * T * BYTES, in ? x + j * team * CH : p.x, in);
+                    else
+                        next[r][j] = in ? x[j * team] : (TX)0.0f;
                 }
             }
             fetch_row = min(fetch_row + R * teams, fetch_stop);
         }
-        ring_commit();
+        if constexpr (RING) ring_commit();
     };
+    if constexpr (RING) {
 #pragma unroll
-    for (int k = 0; k < S - 1; ++k) fetch(k);
+        for (int k = 0; k < S - 1; ++k) fetch(k);
+    } else {
+        fetch(0);
+    }
     int stage = 0, last = S - 1;
     for (uint32_t row = begin; row < end;) {
         const uint32_t g = fdiv(row, p.group), stop = (uint32_t)min((int64_t)end, ((int64_t)g + 1) * p.group.d);
-        Pair f[NV][P], b[NV][P];                // u + w and b of this thread's columns
+        Pair f[P], b[P];                        // u + w and b of this thread's columns
+        {
+            float w[NV][CH], bias[NV][CH];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const uint32_t c = (uint32_t)(lane + j * team) * CH;
-            float w[CH], bias[CH];
+            for (int j = 0; j < NV; ++j) {
+                const uint32_t c = (uint32_t)(lane + j * team) * CH;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) w[i] = 1.0f - p.unit, bias[i] = 0.0f;
-            if (p.w && c < p.cols) load_param<CH>(p.w, p.p_bf16, (int64_t)g * p.ldp + c, w);
-            if (p.b && c < p.cols) load_param<CH>(p.b, p.p_bf16, (int64_t)g * p.ldp + c, bias);
+                for (int i = 0; i < CH; ++i) w[j][i] = 1.0f - p.unit, bias[j][i] = 0.0f;
+                if (p.w && c < p.cols) load_param<CH>(p.w, p.p_bf16, (int64_t)g * p.ldp + c, w[j]);
+                if (p.b && c < p.cols) load_param<CH>(p.b, p.p_bf16, (int64_t)g * p.ldp + c, bias[j]);
+            }
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                f[j][i] = pair_of(p.unit + w[2 * i], p.unit + w[2 * i + 1]);
-                b[j][i] = pair_of(bias[2 * i], bias[2 * i + 1]);
+            for (int k = 0; k < P; ++k) {
+                f[k] = pair_of(p.unit + w[2 * k / CH][2 * k % CH], p.unit + w[(2 * k + 1) / CH][(2 * k + 1) % CH]);
+                b[k] = pair_of(bias[2 * k / CH][2 * k % CH], bias[(2 * k + 1) / CH][(2 * k + 1) % CH]);
             }
         }
         for (uint32_t r0 = row; r0 < stop; r0 += teams * R) {
-            fetch(last);
-            ring_wait<S - 1>();
-            Pair v[R][NV][P];
+            if constexpr (RING) {
+                fetch(last);
+                ring_wait<S - 1>();
+            }
+            Pair v[R][P];
             float s[R], mean[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                Pair sum = 0;
+                float fx[NV][CH];
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    load_pairs<CH>(reinterpret_cast<const TX *>(ring + ((stage * R + r) * NV + j) * T * BYTES), v[r][j]);
+                    if constexpr (RING)
+                        load_chunk<CH>(reinterpret_cast<const TX *>(ring + ((stage * R + r) * NV + j) * T * BYTES), fx[j]);
+                    else
+                        fx[j][0] = (float)next[r][j];
+                }
+                Pair sum = 0;
 #pragma unroll
-                    for (int i = 0; i < P; ++i) sum = add2(sum, v[r][j][i]);
+                for (int k = 0; k < P; ++k) {
+                    v[r][k] = pair_of(fx[2 * k / CH][2 * k % CH], fx[(2 * k + 1) / CH][(2 * k + 1) % CH]);
+                    sum = add2(sum, v[r][k]);
                 }
                 s[r] = pair_sum(sum);
             }
+            if constexpr (!RING) fetch(0);
             last = stage;
             stage = stage + 1 == S ? 0 : stage + 1;
             team_sum<R>(s, team_log2, red, parity);
@@ -371,13 +379,24 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(cons
                 Pair sum = 0;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    const Pair before = sum;
+                    const bool in = (uint32_t)(lane + j * team) * CH < p.cols;
+                    if constexpr (CH == 1) {    // a pair is two chunks: where there is no column it holds the mean
+                        float lo, hi;
+                        pair_split(v[r][j / 2], lo, hi);
+                        if (!in) (j & 1 ? hi : lo) = mean[r];
+                        v[r][j / 2] = pair_of(lo, hi);
+                        if ((j & 1) == 0) continue;
+                        v[r][j / 2] = add2(v[r][j / 2], minus);
+                        sum = fma2(v[r][j / 2], v[r][j / 2], sum);
+                    } else {
+                        const Pair before = sum;
 #pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        v[r][j][i] = add2(v[r][j][i], minus);
-                        sum = fma2(v[r][j][i], v[r][j][i], sum);
+                        for (int k = j * CH / 2; k < (j + 1) * CH / 2; ++k) {
+                            v[r][k] = add2(v[r][k], minus);
+                            sum = fma2(v[r][k], v[r][k], sum);
+                        }
+                        if (!in) sum = before;
                     }
-                    if ((uint32_t)(lane + j * team) * CH >= p.cols) sum = before;       // no column
                 }
                 s[r] = pair_sum(sum);
             }
@@ -394,17 +413,19 @@ __global__ void __launch_bounds__(T, T == 256 ? 3 : 1) layernorm_fwd_kernel(cons
                     if (p.rstd) p.rstd[at] = rstd;
                 }
                 const Pair scale = pair_of(rstd, rstd);
+                float out[NV][CH];
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
+                for (int k = 0; k < P; ++k)
+                    pair_split(fma2(mul2(v[r][k], scale), f[k], b[k]), out[2 * k / CH][2 * k % CH],
+                               out[(2 * k + 1) / CH][(2 * k + 1) % CH]);
 #pragma unroll
-                    for (int i = 0; i < P; ++i) v[r][j][i] = fma2(mul2(v[r][j][i], scale), f[j][i], b[j][i]);
-                    if ((uint32_t)(lane + j * team) * CH < p.cols) store_pairs<CH>(y + j * team * CH, v[r][j]);
-                }
+                for (int j = 0; j < NV; ++j)
+                    if ((uint32_t)(lane + j * team) * CH < p.cols) store_chunk<CH>(y + j * team * CH, out[j]);
             }
         }
         row = stop;
     }
-    ring_wait<0>();
+    if constexpr (RING) ring_wait<0>();
 }
 
 // Floats of a row of dw or db in the workspace: a multiple of 16 bytes.
@@ -473,18 +494,19 @@ __device__ __forceinline__ void flush_grads(const NormBwdParams &p, Pair (&sum_w
     }
 }
 
-// Backward ring: stages of R rows of x and dy, up to three in about 200 KB; without two (rows above 8192 columns
+// Backward ring: stages of R rows of x and dy, up to three (eight of single rows) in about 200 KB; without two (rows above 8192 columns
 // in fp32), and in narrow layouts (no copies of 8 bytes and more), rows are loaded straight into registers.
 template <typename TX, typename TY, int CH, int NV, int R, int T>
 struct BwdRing {
     static constexpr int kStage = R * NV * CH * (int)(sizeof(TX) + sizeof(TY)) * T;
     static constexpr int kFit = 200 * 1024 / kStage;
-    static constexpr int kStages = CH == 1 || kFit < 2 ? 0 : kFit < 3 ? kFit : 3;
+    static constexpr int kMost = R == 1 && T == 256 ? 8 : 3;
+    static constexpr int kStages = CH == 1 || kFit < 2 ? 0 : kFit < kMost ? kFit : kMost;
     static constexpr int kBytes = kStages * kStage;
 };
 
 template <typename TX, typename TY, int CH, int NV, int R, int T, bool ALONE>
-__global__ void __launch_bounds__(T, T == 256 || (CH == 1 && NV == 8) ? 2 : 1) layernorm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(T, T == 256 ? 2 : 1) layernorm_bwd_kernel(const NormBwdParams p) {
     constexpr bool RING = BwdRing<TX, TY, CH, NV, R, T>::kStages > 0;
     constexpr int S = RING ? BwdRing<TX, TY, CH, NV, R, T>::kStages : 1, XB = CH * sizeof(TX), YB = CH * sizeof(TY);
     extern __shared__ __align__(16) uint8_t smem[];
@@ -758,7 +780,7 @@ static int team_of(int64_t chunks, int per, int most) {
 struct SmemAllowed {
     std::atomic<int> bytes[64] = {};
     int operator()(const void *kernel, int want) {
-        if (want <= 48 * 1024) return NOMAS_OK;
+        if (want <= 32 * 1024) return NOMAS_OK;       // with up to 16 KB of static shared memory
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess && dev >= 0 && dev < 64 && bytes[dev].load() >= want) return NOMAS_OK;
@@ -787,9 +809,12 @@ static int pick_row(NormParams &p, cudaStream_t st) {
     const int64_t nv = (chunks + (1 << p.team_log2) - 1) >> p.team_log2;
     if (nv <= 1) return launch_row<TX, TY, CH, 1>(p, st);
     if (nv <= 4) return launch_row<TX, TY, CH, 4>(p, st);
-    if (CH == 8 || nv <= 8) return launch_row<TX, TY, CH, 8>(p, st);
-    if (CH == 4 || nv <= 16) return launch_row<TX, TY, CH, CH == 8 ? 8 : 16>(p, st);
-    return launch_row<TX, TY, CH, CH == 1 ? 64 : 8>(p, st);
+    if (nv <= 8 || CH == 8) return launch_row<TX, TY, CH, 8>(p, st);
+    if constexpr (CH < 8) {
+        if (nv <= 16 || CH == 4) return launch_row<TX, TY, CH, 16>(p, st);
+    }
+    if constexpr (CH == 1) return launch_row<TX, TY, CH, 64>(p, st);
+    return NOMAS_EUNSUPPORTED;                  // not reached: 16384 columns are 16 chunks of 4, 8 of 8
 }
 
 template <typename TX, typename TY, int CH, int NV, int R, int T, bool ALONE>
@@ -799,7 +824,7 @@ static int launch_fwd(NormParams &p, cudaStream_t st) {
     static SmemAllowed allowed;
     const int rc = allowed(reinterpret_cast<const void *>(kernel), kBytes);
     if (rc) return rc;
-    const int64_t teams = T >> p.team_log2, ctas = (int64_t)sm_count() * (T == 512 ? 1 : kBytes > 74 * 1024 ? 2 : 3);
+    const int64_t teams = T >> p.team_log2, ctas = (int64_t)sm_count() * (T == 512 ? 1 : CH == 1 || kBytes > 74 * 1024 ? 2 : 3);
     int64_t share = (p.rows + ctas - 1) / ctas;
     if (share < teams) share = teams;
     p.share = (uint32_t)share;
@@ -807,31 +832,49 @@ static int launch_fwd(NormParams &p, cudaStream_t st) {
     return check_launch("layernorm_fwd_kernel launch");
 }
 
-// Values of a row per thread: 8 with 4 rows at a time, 16 with 2, then teams of 512 threads.
+// Values of a row per thread: 8 with 4 rows at a time, 16 with 2, then teams of 512 threads.  Narrow layouts hold the
+// next rows in registers and take fewer rows at a time.
 template <typename TX, typename TY, int CH>
 static int pick_fwd(NormParams &p, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
-    p.team_log2 = team_of(chunks, 1, 8);
-    if (chunks <= 128) return launch_fwd<TX, TY, CH, 1, 4, 256, false>(p, st);
-    if (chunks <= 256) return launch_fwd<TX, TY, CH, 1, 4, 256, true>(p, st);
-    if (p.cols <= 2048) return launch_fwd<TX, TY, CH, 8 / CH, 4, 256, true>(p, st);
-    if (p.cols <= 4096) return launch_fwd<TX, TY, CH, 16 / CH, 2, 256, true>(p, st);
-    p.team_log2 = 9;
-    if (p.cols <= 8192) return launch_fwd<TX, TY, CH, 16 / CH, 2, 512, true>(p, st);
-    return launch_fwd<TX, TY, CH, 32 / CH, 1, 512, true>(p, st);
+    constexpr int kLeast = CH == 1 ? 2 : 1;     // pairs of values
+    p.team_log2 = team_of(chunks, kLeast, 8);
+    if (chunks <= kLeast * 128) return launch_fwd<TX, TY, CH, kLeast, 4, 256, false>(p, st);
+    if (chunks <= kLeast * 256) return launch_fwd<TX, TY, CH, kLeast, 4, 256, true>(p, st);
+    if constexpr (CH == 1) {
+        if (p.cols <= 2048) return launch_fwd<TX, TY, 1, 8, 2, 256, true>(p, st);
+        p.team_log2 = 9;
+        if (p.cols <= 4096) return launch_fwd<TX, TY, 1, 8, 2, 512, true>(p, st);
+        if (p.cols <= 8192) return launch_fwd<TX, TY, 1, 16, 1, 512, true>(p, st);
+        return launch_fwd<TX, TY, 1, 32, 1, 512, true>(p, st);
+    } else {
+        if (p.cols <= 2048) return launch_fwd<TX, TY, CH, 8 / CH, 4, 256, true>(p, st);
+        if (p.cols <= 4096) return launch_fwd<TX, TY, CH, 16 / CH, 2, 256, true>(p, st);
+        p.team_log2 = 9;
+        if (p.cols <= 8192) return launch_fwd<TX, TY, CH, 16 / CH, 2, 512, true>(p, st);
+        return launch_fwd<TX, TY, CH, 32 / CH, 1, 512, true>(p, st);
+    }
+}
+
+template <typename TX, typename TY, int CH>
+static int row_or_share(NormParams &p, cudaStream_t st) {
+    // few rows: latency, not bandwidth.  Groups of few rows: a share would wait for each group's parameters and leave
+    // most of its rows' places empty (26400 x 1024 in groups of one row: 188 us by shares)
+    const int64_t chunks = (p.cols + CH - 1) / CH, teams = chunks >= kNormThreads ? 1 : kNormThreads / chunks;
+    const bool few = p.rows <= (uint32_t)(2 * sm_count()) || p.group.d < 4 * teams;
+    return few ? pick_row<TX, TY, CH>(p, st) : pick_fwd<TX, TY, CH>(p, st);
 }
 
 template <typename TX, typename TY>
 static int any_fwd(NormParams &p, bool wide, cudaStream_t st) {
     constexpr int CH = sizeof(TX) == 2 && sizeof(TY) == 2 ? 8 : 4;     // 16 bytes of the wider type
-    if (!wide) return pick_row<TX, TY, 1>(p, st);
-    // few rows: latency, not bandwidth
-    return p.rows <= (uint32_t)(2 * sm_count()) ? pick_row<TX, TY, CH>(p, st) : pick_fwd<TX, TY, CH>(p, st);
+    return wide ? row_or_share<TX, TY, CH>(p, st) : row_or_share<TX, TY, 1>(p, st);
 }
 
-// Shares of the backward pass: the CTAs that the device holds at once, each with at least a round of rows.
-static void bwd_shares(int64_t rows, int64_t cols, int64_t *share, int64_t *ctas) {
-    const int64_t most = 2 * (int64_t)sm_count(), least = cols <= 512 ? 16 : 4;
+// Shares of the backward pass: the CTAs that the device holds at once (`per_sm` on an SM), each with at least a round
+// of rows.
+static void bwd_shares(int64_t rows, int64_t cols, int per_sm, int64_t *share, int64_t *ctas) {
+    const int64_t most = per_sm * (int64_t)sm_count(), least = cols <= 512 ? 16 : 4;
     int64_t s = (rows + most - 1) / most;
     if (s < least) s = least;
     *share = s;
@@ -866,8 +909,12 @@ static int pick_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
     constexpr int kLeast = CH == 1 ? 2 : 1;     // pairs of values
     p.team_log2 = team_of(chunks, kLeast, 8);
-    if (chunks <= kLeast * 128) return launch_bwd<TX, TY, CH, kLeast, 4, 256, false>(p, ctas, st);
-    if (chunks <= kLeast * 256) return launch_bwd<TX, TY, CH, kLeast, 4, 256, true>(p, ctas, st);
+    // groups of few rows: batches stay inside a group, so one row of a team at a time
+    const bool small = p.group.d <= 2 * (kNormThreads >> p.team_log2);
+    if (chunks <= kLeast * 128)
+        return small ? launch_bwd<TX, TY, CH, kLeast, 1, 256, false>(p, ctas, st) : launch_bwd<TX, TY, CH, kLeast, 4, 256, false>(p, ctas, st);
+    if (chunks <= kLeast * 256)
+        return small ? launch_bwd<TX, TY, CH, kLeast, 1, 256, true>(p, ctas, st) : launch_bwd<TX, TY, CH, kLeast, 4, 256, true>(p, ctas, st);
     if constexpr (CH == 1) {
         if (p.cols <= 2048) return launch_bwd<TX, TY, 1, 8, 1, 256, true>(p, ctas, st);
         p.team_log2 = 9;
@@ -925,7 +972,7 @@ extern "C" int nomas_layernorm_fwd(const void *x, int64_t rows, int64_t cols, in
 extern "C" size_t nomas_layernorm_workspace_bytes(int64_t rows, int64_t cols, int64_t rows_per_group) {
     if (check_norm(rows, cols, rows_per_group)) return 0;
     int64_t share, ctas;
-    bwd_shares(rows, cols, &share, &ctas);
+    bwd_shares(rows, cols, 2, &share, &ctas);
     const size_t n = ctas > 1 ? (size_t)ctas * 4 * (size_t)part_pitch(cols) * sizeof(float) : 0;
     return n < 16 ? 16 : n;
 }
@@ -958,8 +1005,9 @@ extern "C" int nomas_layernorm_bwd(const void *dy, int64_t lddy, int y_dtype, co
         return NOMAS_OK;
     }
     NormBwdParams p{};
+    const bool wide = cols % 8 == 0 && wide_ok(dy, lddy) && wide_ok(x, ldx) && wide_ok(w, ldp) && wide_ok(dx, lddx);
     int64_t share, ctas;
-    bwd_shares(rows, cols, &share, &ctas);
+    bwd_shares(rows, cols, cols > (wide ? 4096 : 2048) ? 1 : 2, &share, &ctas);    // 512 threads: one CTA an SM
     p.dy = dy, p.x = x, p.w = w, p.mean = mean, p.rstd = rstd, p.dx = dx, p.dw = dw, p.db = db;
     p.part = static_cast<float *>(workspace);
     p.lddy = lddy, p.ldx = ldx, p.lddx = lddx, p.ldp = ldp, p.ldg = ldg;
@@ -968,7 +1016,6 @@ extern "C" int nomas_layernorm_bwd(const void *dy, int64_t lddy, int y_dtype, co
     p.p_bf16 = p_dtype == NOMAS_DTYPE_BF16;
     p.unit = unit_offset && w ? 1.0f : 0.0f;
     p.grad_wide = wide_ok(dw, ldg) && wide_ok(db, ldg);
-    const bool wide = cols % 8 == 0 && wide_ok(dy, lddy) && wide_ok(x, ldx) && wide_ok(w, ldp) && wide_ok(dx, lddx);
     if (x_dtype == NOMAS_DTYPE_BF16)
         return y_dtype == NOMAS_DTYPE_BF16 ? any_bwd<__nv_bfloat16, __nv_bfloat16>(p, wide, ctas, st)
                                            : any_bwd<__nv_bfloat16, float>(p, wide, ctas, st);
