@@ -474,8 +474,8 @@ int nomas_w4_quantize(const void *w, int64_t n_out, int64_t k_in, int64_t ldw, i
 /* Dequantise into bf16 weights w [N][K] (dense). */
 int nomas_w4_dequant(const uint8_t *codes, const void *scales, int group, int64_t n_out, int64_t k_in, void *w,
                      nomas_stream stream);
-/* Bytes of the workspace of a nomas_w4a16_linear call with m rows: 0 for up to NOMAS_W4_FEW_ROWS rows (the
- * weights are widened in registers), else N * K * 2 for the transient bf16 weights of the tensor-core GEMM. */
+/* Bytes of the workspace of a nomas_w4a16_linear call with m rows: 0 for few rows (the weights are
+ * widened in registers: up to NOMAS_W4_FEW_ROWS rows always), else N * K * 2 for the transient bf16 weights of the tensor-core GEMM. */
 #define NOMAS_W4_FEW_ROWS 64
 size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in);
 /* y [M][N] = x [M][K] W^T.  workspace may be NULL when nomas_w4a16_workspace_bytes gives 0; status as for

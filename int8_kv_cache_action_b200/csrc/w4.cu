@@ -3,12 +3,12 @@
 // Kernels:
 //   w4_quantize_kernel  one warp per (row, group)
 //   w4_dequant_kernel   bf16(code * scale), 32 weights per thread (HBM-bound)
-//   w4_rows_kernel      y = x W^T for up to NOMAS_W4_FEW_ROWS rows of x, every code read once: bound by the codes'
-//                       bytes, so the weights are widened in registers and go straight into the register
-//                       form of the tensor-core product (m16n8k16, 16 rows of W by 8 rows of x): one
-//                       instruction per 8 weights of a lane, where fp32 products would need one per
-//                       weight and row of x.  tcgen05 would want the widened weights in shared memory
-//                       first; it takes over (w4_dequant_kernel, nomas_linear_bf16) for more rows.
+//   w4_rows_kernel      y = x W^T for few rows of x, every code read once for 32 of them: bound by the codes'
+//                       bytes and by widening them, about 20 instructions a word of 8.  The weights are widened in
+//                       registers and go straight into the register form of the tensor-core product (m16n8k16,
+//                       16 rows of W by 8 rows of x): one instruction per 8 weights of a lane, where fp32
+//                       products would need one per weight and row of x.  tcgen05 would want the widened weights
+//                       in shared memory first; it takes over (w4_dequant_kernel, nomas_linear_bf16) for more rows.
 #include "common.cuh"
 
 namespace nomas {
@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_ke
     constexpr int LD = 16 * RT + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+    const int m0 = blockIdx.y * 8 * NT, m = min(p.m - m0, 8 * NT);      // rows of x
     const int chunks = p.k >> 7, tail = p.k & 127;
     // this CTA's rows: 32-bit offsets from the first; rows past the end repeat the last one, and their products go
     // nowhere
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_ke
         }
     const __nv_bfloat16 *xr[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) xr[i] = p.x + (int64_t)min(8 * i + g, p.m - 1) * p.ldx + 32 * t;
+    for (int i = 0; i < NT; ++i) xr[i] = p.x + (int64_t)(m0 + min(8 * i + g, m - 1)) * p.ldx + 32 * t;
     float acc[RT][NT][4];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -188,16 +189,16 @@ __global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_ke
 #pragma unroll
             for (int j = 0; j < 4; ++j) mine[(8 * i + 2 * t + (j & 1)) * LD + 16 * r + 8 * (j >> 1) + g] = acc[r][i][j];
     __syncthreads();
-    for (int e = threadIdx.x; e < p.m * 16 * RT; e += 32 * WARPS) {
+    for (int e = threadIdx.x; e < m * 16 * RT; e += 32 * WARPS) {
         const int row = e / (16 * RT), col = e % (16 * RT);
         if (n0 + col >= p.n) continue;
         float s = red[row * LD + col];
 #pragma unroll
         for (int w = 1; w < WARPS; ++w) s += red[(w * 8 * NT + row) * LD + col];
         if (p.y_bf16)
-            static_cast<__nv_bfloat16 *>(p.y)[(int64_t)row * p.ldy + n0 + col] = __float2bfloat16_rn(s);
+            static_cast<__nv_bfloat16 *>(p.y)[(int64_t)(m0 + row) * p.ldy + n0 + col] = __float2bfloat16_rn(s);
         else
-            static_cast<float *>(p.y)[(int64_t)row * p.ldy + n0 + col] = s;
+            static_cast<float *>(p.y)[(int64_t)(m0 + row) * p.ldy + n0 + col] = s;
     }
 }
 
@@ -261,6 +262,10 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16 *w
 // host
 // ------------------------------------------------------------------------------------------------
 
+// Rows of x that go to w4_rows_kernel: the GEMM's 128 x 256 tiles leave most SMs idle below 4096 rows of W (100 rows,
+// 2048 x 2048: 19 us against 12; 2048 -> 12288: 34 against 52 the other way).
+static bool w4_few(int64_t m, int64_t n_out) { return m <= NOMAS_W4_FEW_ROWS || (m <= 128 && n_out <= 4096); }
+
 static int group_log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
 
 static int check_w4(const void *codes, const void *scales, int group, int64_t n_out, int64_t k_in) {
@@ -284,21 +289,30 @@ template <int NT, int RT, int WARPS>
 static int launch_w4_rows(const W4Params &p, cudaStream_t st) {
     constexpr int kBytes = WARPS * 8 * NT * (16 * RT + 1) * (int)sizeof(float);
     static_assert(kBytes <= 48 * 1024, "above 48 KB a kernel needs an attribute");
-    w4_rows_kernel<NT, RT, WARPS><<<(unsigned)((p.n + 16 * RT - 1) / (16 * RT)), 32 * WARPS, kBytes, st>>>(p);
+    // more rows of x than a CTA's registers sum: as many CTAs, which find the codes in L2
+    const dim3 grid((unsigned)((p.n + 16 * RT - 1) / (16 * RT)), (unsigned)((p.m + 8 * NT - 1) / (8 * NT)));
+    w4_rows_kernel<NT, RT, WARPS><<<grid, 32 * WARPS, kBytes, st>>>(p);
     return check_launch("w4_rows_kernel launch");
 }
 
-// 32 rows of W a CTA of 4 warps when that gives every SM two CTAs (x is read half as often); narrower matrices take 16
-// rows and split long rows over more warps, so that the codes on their way still fill the machine (5 x 8192 -> 2048:
-// 6.0 us with 16 warps, 6.9 with 8, 9.9 with 4; 1 x 2048 -> 12288: 6.0 with 4, 6.7 with 8; with 32 rows and 4 warps 13.5
-// and 6.3).
+// Rows of W and warps of a CTA.  Long rows of wide matrices: 32 rows (x is read half as often) by 8 warps; else as
+// many warps to a row as make some 2000 to 3000 in all, so that the codes on their way fill the machine, and 32 rows by 4
+// warps where rows of x make x the larger part.  Measured in us, (rows / 16, warps):
+//             (1,4)  (1,8) (1,16)  (2,4)  (2,8)                        (1,4)  (1,8) (1,16)  (2,4)  (2,8)
+//    1 x 2048 -> 2048   3.6   2.9    2.8    4.8    3.8     30 x 2048 -> 2048   6.3   5.5    5.7   10.1    7.5
+//    1 x 8192 -> 2048   9.8   6.3    5.3   13.5    9.6     30 x 8192 -> 2048  21.3  14.9   13.8   38.5   23.6
+//    1 x 4096 -> 4096   6.0   5.0    6.1    7.9    6.0     30 x 4096 -> 4096  14.0  13.7   15.7   18.6   12.8
+//    1 x 8192 -> 8192  17.7  19.3   20.9   22.5   14.7     30 x 8192 -> 8192  45.5  46.9   52.0   45.5   31.7
+//    1 x 2048 -> 12288  6.2   7.0   10.6    6.7    6.8     30 x 2048 -> 12288 24.1  21.2   26.4   13.4   17.6
+//    1 x 8192 -> 28001 39.3  40.9   61.8   35.5   35.7     30 x 8192 -> 28001  133   137    155    117     92
 template <int NT>
 static int pick_w4_rows(const W4Params &p, cudaStream_t st) {
-    if constexpr (NT <= 4) {
-        if (p.n >= 64 * (int64_t)sm_count()) return launch_w4_rows<NT, 2, 4>(p, st);
-        if (p.k >= 4096) return launch_w4_rows<NT, 1, 16>(p, st);
-    }
-    return p.k >= 2048 ? launch_w4_rows<NT, 1, 8>(p, st) : launch_w4_rows<NT, 1, 4>(p, st);
+    const int64_t tiles = (p.n + 15) / 16;
+    if (p.k >= 4096 && tiles >= (NT == 1 ? 512 : 256)) return launch_w4_rows<NT, 2, 8>(p, st);
+    if (tiles >= 640) return NT == 1 ? launch_w4_rows<NT, 1, 4>(p, st) : launch_w4_rows<NT, 2, 4>(p, st);
+    if (p.k < 1024) return launch_w4_rows<NT, 1, 4>(p, st);
+    if (tiles >= 256) return NT == 4 ? launch_w4_rows<NT, 2, 8>(p, st) : launch_w4_rows<NT, 1, 8>(p, st);
+    return p.k >= (NT == 1 ? 2048 : 4096) ? launch_w4_rows<NT, 1, 16>(p, st) : launch_w4_rows<NT, 1, 8>(p, st);
 }
 
 }  // namespace nomas
@@ -331,7 +345,7 @@ extern "C" int nomas_w4_dequant(const uint8_t *codes, const void *scales, int gr
 }
 
 extern "C" size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in) {
-    if (m <= NOMAS_W4_FEW_ROWS || n_out < 1 || k_in < 1) return 0;
+    if (n_out < 1 || k_in < 1 || w4_few(m, n_out)) return 0;
     return (size_t)n_out * (size_t)k_in * 2;
 }
 
@@ -344,12 +358,12 @@ extern "C" int nomas_w4a16_linear(const void *x, int64_t m, int64_t k_in, int64_
     if (ldx < k_in || ldx % 8 != 0 || ldy < n_out) return NOMAS_EINVAL;
     if (y_dtype != NOMAS_DTYPE_F32 && y_dtype != NOMAS_DTYPE_BF16) return NOMAS_EINVAL;
     if (m >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
-    if (m > NOMAS_W4_FEW_ROWS && (!workspace || !aligned16(workspace))) return NOMAS_EINVAL;
+    if (!w4_few(m, n_out) && (!workspace || !aligned16(workspace))) return NOMAS_EINVAL;
     if (m == 0) return NOMAS_OK;
     DeviceScope dev(codes);
     if (dev.rc) return dev.rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (m > NOMAS_W4_FEW_ROWS) {
+    if (!w4_few(m, n_out)) {
         rc = enqueue_w4_dequant(codes, scales, group, n_out, k_in, workspace, st);
         if (rc) return rc;
         return nomas_linear_bf16(x, m, k_in, ldx, workspace, n_out, k_in, y, ldy, y_dtype, status, stream);
@@ -366,6 +380,5 @@ extern "C" int nomas_w4a16_linear(const void *x, int64_t m, int64_t k_in, int64_
     p.y_bf16 = y_dtype == NOMAS_DTYPE_BF16;
     if (m <= 8) return pick_w4_rows<1>(p, st);
     if (m <= 16) return pick_w4_rows<2>(p, st);
-    if (m <= 32) return pick_w4_rows<4>(p, st);
-    return pick_w4_rows<8>(p, st);
+    return pick_w4_rows<4>(p, st);
 }
