@@ -460,6 +460,49 @@ def measure_linear(dev, reps=10):
     return out
 
 
+def measure_block_ops(dev, reps=20):
+    """The operators around the attention on the production segment (30 frames of 22 x 40 tokens, hidden 2048,
+    16 heads x 128): modulation of every frame from its embedding (4-bit linear), the modulated layer norm and its
+    backward pass, and the rotary positions of q and k in the fused QKV projection's buffer.  Device time of a call
+    among others (CUDA events, warm, inputs above L2 except the linear layer's), and its bytes."""
+    import torch
+    from int8_kv_cache_action_b200.runtime import AxisRope, Int4Linear, layer_norm, layer_norm_backward, rope_grid
+    frames, gh, gw, hidden, heads, d = 30, 22, 40, 2048, 16, 128
+    tokens, per_frame = frames * gh * gw, gh * gw
+    g = torch.Generator(device=dev).manual_seed(78)
+
+    def randn(*shape, scale=1.0):
+        return (torch.randn(*shape, generator=g, device=dev) * scale).to(torch.bfloat16)
+
+    lin = Int4Linear.from_weights(randn(6 * hidden, hidden, scale=0.02))
+    emb, x, dy, qkv = randn(frames, hidden), randn(tokens, hidden), randn(tokens, hidden), randn(tokens, 3, heads, d)
+    mod = lin(emb)
+    shift, scale = mod[:, :hidden], mod[:, hidden:2 * hidden]
+    _, mean, rstd = layer_norm(x, scale, shift, rows_per_group=per_frame, unit_offset=True, want_stats=True)
+    rope, grid, qk = AxisRope(d, (16, 56, 56)), rope_grid(gh, gw), (qkv[:, 0], qkv[:, 1])
+    act = tokens * hidden * 2
+    calls = {"modulation_30_frames": (lambda: lin(emb), lin.codes.numel() + 2 * lin.scales.numel() + mod.numel() * 2),
+             "modulation_1_vector": (lambda: lin(emb[:1]), lin.codes.numel() + 2 * lin.scales.numel()),
+             "layer_norm": (lambda: layer_norm(x, scale, shift, rows_per_group=per_frame, unit_offset=True), 2 * act),
+             "layer_norm_backward": (lambda: layer_norm_backward(dy, x, mean, rstd, scale, rows_per_group=per_frame,
+                                                                 unit_offset=True), 3 * act),
+             "rope_q_k": (lambda: rope(qk, grid=grid, out=qk), 4 * act)}
+    out = {}
+    for name, (fn, nbytes) in calls.items():
+        for _ in range(3):
+            fn()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        e0.record()
+        for _ in range(reps):
+            fn()
+        e1.record()
+        torch.cuda.synchronize()
+        us = e0.elapsed_time(e1) / reps * 1e3
+        out[name] = {"us": us, "gbs": nbytes / us / 1e3}
+    return out
+
+
 def per_config(args):
     """One JSON line per config: the attention call (its mode: dense, or sparse for C3) and the mask
     build of that mode timed with CUDA events over back-to-back calls after 3 warm-ups, and the
@@ -608,6 +651,9 @@ def main():
                     help="head_dim-128 attention kernel: 0 chosen per call, 1 one query block per CTA, 2 block pairs")
     ap.add_argument("--linear-only", action="store_true",
                     help="print one line with the INT8-weight linear layer on the DiT shapes only")
+    ap.add_argument("--block-ops", action="store_true",
+                    help="print one line with the operators around the attention (modulation, layer norm, rotary "
+                         "positions) on the production segment only")
     args = ap.parse_args()
     rank = int(os.environ.get("RANK", 0))
     world = int(os.environ.get("WORLD_SIZE", 1))
@@ -639,6 +685,13 @@ def main():
         N.nomas_set_attn_kernel(args.attn_kernel)
     if args.per_config:
         per_config(args)
+        return
+    if args.block_ops:
+        import torch
+        peak = pk.get("hbm_gbs", FALLBACK_PEAKS["hbm_gbs"])
+        ops = measure_block_ops(torch.device("cuda", 0), reps=args.reps or 20)
+        print(json.dumps({"block_ops": ops, "peak_hbm_gbs": peak, "peak_kind": pk_kind,
+                          "frac": {k: v["gbs"] / peak for k, v in ops.items()}}))
         return
     if args.linear_only:
         import torch
