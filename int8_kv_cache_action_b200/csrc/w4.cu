@@ -2,7 +2,7 @@
 //
 // Kernels:
 //   w4_quantize_kernel  one warp per (row, group)
-//   w4_dequant_kernel   bf16(code * scale), 32 weights per thread (HBM-bound)
+//   w4_dequant_kernel   bf16(code * scale), bound by the weights it writes
 //   w4_rows_kernel      y = x W^T for few rows of x, every code read once for 32 of them: bound by the codes'
 //                       bytes and by widening them, about 20 instructions a word of 8.  The weights are widened in
 //                       registers and go straight into the register form of the tensor-core product (m16n8k16,
@@ -35,6 +35,14 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with D = A B.
+__device__ __forceinline__ void mma_16x8x16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                  uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 struct W4Params {
@@ -121,10 +129,6 @@ __global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_ke
         for (int r = 0; r < RT; ++r) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) s[r][h] = __halves2bfloat162(v.f[r][h], v.f[r][h]);
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) part[r][i][j] = 0.0f;
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -145,14 +149,14 @@ __global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_ke
                 const uint32_t x2 = __byte_perm(xv.y, xv.w, 0x5410), x3 = __byte_perm(xv.y, xv.w, 0x7632);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    mma_16x8x16(part[r][i], u[r][0][0], u[r][1][0], u[r][0][1], u[r][1][1], x0, x1);
+                    if (q == 0 || !WHOLE)
+                        mma_16x8x16_first(part[r][i], u[r][0][0], u[r][1][0], u[r][0][1], u[r][1][1], x0, x1);
+                    else
+                        mma_16x8x16(part[r][i], u[r][0][0], u[r][1][0], u[r][0][1], u[r][1][1], x0, x1);
                     mma_16x8x16(part[r][i], u[r][0][2], u[r][1][2], u[r][0][3], u[r][1][3], x2, x3);
                     if (q == 3 || !WHOLE) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            acc[r][i][j] += part[r][i][j];
-                            part[r][i][j] = 0.0f;
-                        }
+                        for (int j = 0; j < 4; ++j) acc[r][i][j] += part[r][i][j];
                     }
                 }
             }
@@ -161,10 +165,12 @@ __global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_ke
 
     W4Codes<RT> now, next;
     if (warp < chunks) load(now, warp);
-    for (int c = warp; c < chunks; c += WARPS) {
+    for (int c = warp; c < chunks; c += 2 * WARPS) {
         if (c + WARPS < chunks) load(next, c + WARPS);
         multiply(now, c, true);
-        now = next;
+        if (c + WARPS >= chunks) break;
+        if (c + 2 * WARPS < chunks) load(now, c + 2 * WARPS);
+        multiply(next, c + WARPS, true);
     }
     // the last 32, 64 or 96 columns: lanes past them hold zeros
     if (tail && warp == chunks % WARPS) {
@@ -202,25 +208,30 @@ __global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_ke
     }
 }
 
-__global__ void __launch_bounds__(256) w4_dequant_kernel(const uint8_t *codes, const __nv_bfloat16 *scales, int64_t total32,
-                                                         int32_t k32, int32_t groups, int32_t group_log2,
-                                                         __nv_bfloat16 *w) {
-    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total32; i += stride) {
-        const int64_t row = i / k32;
-        const int32_t col = (int32_t)(i - row * k32) * 32;
-        const __nv_bfloat16 f = scales[row * groups + (col >> group_log2)];
-        const __nv_bfloat162 s = __halves2bfloat162(f, f);
-        const uint4 c = load_stream(codes + i * 16);
-        const uint32_t word[4] = {c.x, c.y, c.z, c.w};
-        uint4 *dst = reinterpret_cast<uint4 *>(w + i * 32);
+// A word of 8 codes a thread: 16 bytes out, whole lines a warp.
+constexpr int kDequantUnroll = 4;
+
+__global__ void __launch_bounds__(256) w4_dequant_kernel(const uint32_t *codes, const __nv_bfloat16 *scales, uint32_t words,
+                                                         FastDiv row_words, int32_t groups, int32_t group_log2, uint4 *w) {
+    const uint32_t first = blockIdx.x * (256 * kDequantUnroll) + threadIdx.x;
+    uint32_t word[kDequantUnroll];
+    __nv_bfloat16 f[kDequantUnroll];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t u[4];
-            w4_widen(word[q], s, u);
-            dst[q] = make_uint4(__byte_perm(u[0], u[1], 0x5410), __byte_perm(u[2], u[3], 0x5410),
-                                __byte_perm(u[0], u[1], 0x7632), __byte_perm(u[2], u[3], 0x7632));
-        }
+    for (int u = 0; u < kDequantUnroll; ++u) {
+        const uint32_t i = first + u * 256;
+        if (i >= words) continue;
+        const uint32_t row = fdiv(i, row_words), col = (i - row * row_words.d) * 8;
+        word[u] = __ldg(codes + i);
+        f[u] = scales[(int64_t)row * groups + (col >> group_log2)];
+    }
+#pragma unroll
+    for (int u = 0; u < kDequantUnroll; ++u) {
+        const uint32_t i = first + u * 256;
+        if (i >= words) continue;
+        uint32_t v[4];
+        w4_widen(word[u], __halves2bfloat162(f[u], f[u]), v);
+        w[i] = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                          __byte_perm(v[2], v[3], 0x7632));
     }
 }
 
@@ -271,17 +282,17 @@ static int group_log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 :
 static int check_w4(const void *codes, const void *scales, int group, int64_t n_out, int64_t k_in) {
     if (!codes || !scales || !aligned16(codes) || !aligned16(scales) || group_log2_of(group) < 0) return NOMAS_EINVAL;
     if (n_out < 1 || k_in < 32 || k_in % 32 != 0) return NOMAS_EINVAL;
-    if (n_out >= (int64_t)1 << 31 || k_in >= (int64_t)1 << 30) return NOMAS_EUNSUPPORTED;
+    // 32-bit offsets: of 32 rows in w4_rows_kernel, of words in w4_dequant_kernel
+    if (n_out >= (int64_t)1 << 31 || k_in >= (int64_t)1 << 26 || n_out * (k_in / 8) >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
     return NOMAS_OK;
 }
 
 static int enqueue_w4_dequant(const uint8_t *codes, const void *scales, int group, int64_t n_out, int64_t k_in, void *w,
                               cudaStream_t st) {
-    const int64_t total = n_out * (k_in / 32), most = (int64_t)sm_count() * 8;
-    const int64_t blocks = (total + 255) / 256;
-    w4_dequant_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(
-        codes, static_cast<const __nv_bfloat16 *>(scales), total, (int32_t)(k_in / 32), (int32_t)((k_in + group - 1) / group),
-        group_log2_of(group), static_cast<__nv_bfloat16 *>(w));
+    const int64_t words = n_out * (k_in / 8), per_cta = 256 * kDequantUnroll;
+    w4_dequant_kernel<<<(unsigned)((words + per_cta - 1) / per_cta), 256, 0, st>>>(
+        reinterpret_cast<const uint32_t *>(codes), static_cast<const __nv_bfloat16 *>(scales), (uint32_t)words,
+        make_fastdiv((uint32_t)(k_in / 8)), (int32_t)((k_in + group - 1) / group), group_log2_of(group), static_cast<uint4 *>(w));
     return check_launch("w4_dequant_kernel launch");
 }
 
