@@ -474,10 +474,12 @@ int nomas_w4_quantize(const void *w, int64_t n_out, int64_t k_in, int64_t ldw, i
 /* Dequantise into bf16 weights w [N][K] (dense). */
 int nomas_w4_dequant(const uint8_t *codes, const void *scales, int group, int64_t n_out, int64_t k_in, void *w,
                      nomas_stream stream);
-/* Bytes of the workspace of a nomas_w4a16_linear call with m rows: 0 for few rows (the weights are
- * widened in registers: up to NOMAS_W4_FEW_ROWS rows always), else N * K * 2 for the transient bf16 weights of the tensor-core GEMM. */
+/* Bytes of the workspace of a nomas_w4a16_linear call with m rows and results of y_dtype: 0 for few rows (the
+ * weights are widened in registers: up to NOMAS_W4_FEW_ROWS rows always), else the transient bf16 weights of the
+ * tensor-core GEMM (N * K * 2 bytes, rounded up to 256) and, for fp32 results of more than 1024 columns, up to four
+ * partial results: the tensor core truncates its sums, so runs of 1024 columns are added up in rounded fp32. */
 #define NOMAS_W4_FEW_ROWS 64
-size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in);
+size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in, int y_dtype);
 /* y [M][N] = x [M][K] W^T.  workspace may be NULL when nomas_w4a16_workspace_bytes gives 0; status as for
  * nomas_linear_bf16.  Runs on the device that holds the codes. */
 int nomas_w4a16_linear(const void *x, int64_t m, int64_t k_in, int64_t ldx, const uint8_t *codes, const void *scales,

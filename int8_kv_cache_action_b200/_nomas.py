@@ -141,7 +141,7 @@ _sigs = {
                                            ctypes.c_int, _i64, ctypes.c_int, _p, _p, _p, _i64, _p, _p, _i64, _p, _p]),
     "nomas_w4_quantize": (ctypes.c_int, [_p, _i64, _i64, _i64, ctypes.c_int, _p, _p, _p]),
     "nomas_w4_dequant": (ctypes.c_int, [_p, _p, ctypes.c_int, _i64, _i64, _p, _p]),
-    "nomas_w4a16_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "nomas_w4a16_workspace_bytes": (_sz, [_i64, _i64, _i64, ctypes.c_int]),
     "nomas_w4a16_linear": (ctypes.c_int, [_p, _i64, _i64, _i64, _p, _p, ctypes.c_int, _i64, _p, _i64, ctypes.c_int,
                                           _p, _p, _p]),
 }
@@ -396,8 +396,8 @@ def nomas_w4_dequant(codes, scales, group, n_out, k_in, w, stream=0):
     return lib.nomas_w4_dequant(codes, scales, group, n_out, k_in, w, stream or None)
 
 
-def nomas_w4a16_workspace_bytes(m, n_out, k_in):
-    return lib.nomas_w4a16_workspace_bytes(m, n_out, k_in)
+def nomas_w4a16_workspace_bytes(m, n_out, k_in, y_dtype=NOMAS_DTYPE_BF16):
+    return lib.nomas_w4a16_workspace_bytes(m, n_out, k_in, y_dtype)
 
 
 def nomas_w4a16_linear(x, m, k_in, ldx, codes, scales, group, n_out, y, ldy, y_dtype, workspace, status, stream=0):

@@ -8,7 +8,11 @@
 //                       registers and go straight into the register form of the tensor-core product (m16n8k16,
 //                       16 rows of W by 8 rows of x): one instruction per 8 weights of a lane, where fp32
 //                       products would need one per weight and row of x.  tcgen05 would want the widened weights
-//                       in shared memory first; it takes over (w4_dequant_kernel, nomas_linear_bf16) for more rows.
+//                       in shared memory first; for more rows of x others take over:
+//   w4_tile_kernel      the same by tcgen05, the weights widened into TMEM
+//   w4_dequant_kernel and nomas_linear_bf16, above 64 or 128 rows
+#include <atomic>
+
 #include "common.cuh"
 
 namespace nomas {
@@ -208,6 +212,284 @@ __global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_ke
     }
 }
 
+// ------------------------------------------------------------------------------------------------
+// few rows of x by tcgen05
+// ------------------------------------------------------------------------------------------------
+// A CTA: 128 rows of W by a share of the columns, in slabs of 256 whose codes TMA brings some slabs ahead (rows are far
+// apart: loaded by thread, one row each, a slab took 2 us); the CTAs of a cluster share the columns of the same rows.
+// Eight warps widen: a thread takes 64 columns of its row per half slab and writes them straight to TMEM, where
+// tcgen05.mma takes its A operand (a row a lane, two columns of W a 32-bit column), so the widened weights never pass
+// through shared memory; x is the B operand, K-major with the 128-byte swizzle, its columns in the order in which words
+// widen.  A ninth warp issues copies and products (issued by a widening warp, that warp held up the others: 1850 cycles
+// a half slab instead of 700).  The tensor core truncates its sums, so the sums of every 512 columns leave TMEM for fp32
+// additions in registers.  Two buffers of A and x, and two CTAs an SM, hide each other's waits.  At the end the CTAs of
+// a cluster add their sums up through distributed shared memory, in rank order.  Bound by the tensor core's reading of A
+// from TMEM, 64 cycles and more for 16 columns whatever the rows of x, so it pays from about 17 of them on.
+constexpr int kTileRows = 128, kSlab = 256, kTileThreads = 256;        // threads that widen; one more warp issues
+constexpr uint32_t kTileTmem = 256, kTileD = 128;      // TMEM columns of a CTA: A at 0, D at kTileD
+constexpr int kTileStage = kTileRows * kSlab / 2;
+// Scales of kScaleSlabs slabs wait in shared memory, a row's at a pitch of an odd number of 4-byte banks.
+constexpr int kScaleSlabs = 8, kScalePitch = kScaleSlabs * kSlab / 32 + 2;
+
+struct W4Tile {
+    W4Params p;
+    int32_t slabs, share;                      // slabs of K, of a CTA
+    int *err;
+    uint64_t timeout_ns;
+};
+
+// 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16f_sync(uint32_t addr, float (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : NOMAS_F8(0), NOMAS_F8(8)
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void w4_cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t w4_cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t w4_cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ float w4_load_of(uint32_t shared_addr, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(shared_addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void w4_store(const W4Params &p, int64_t row, int64_t col, float v) {
+    if (p.y_bf16)
+        static_cast<__nv_bfloat16 *>(p.y)[row * p.ldy + col] = __float2bfloat16_rn(v);
+    else
+        static_cast<float *>(p.y)[row * p.ldy + col] = v;
+}
+
+// NX: rows of x of a CTA, 32 or 64 (the product's N).
+template <int NX>
+struct TileSmem {
+    static constexpr int kStages = NX == 64 ? 3 : 4;           // two CTAs fit an SM
+    static constexpr int kX = NX * kSlab * 2;                  // a slab of x, later the CTA's sums
+    static constexpr int kScales = kTileRows * kScalePitch * 2;
+    static constexpr int kBytes = kStages * kTileStage + kX + kScales + 1024;      // slack for 1024-byte alignment
+};
+
+template <int NX>
+__global__ void __launch_bounds__(kTileThreads + 32, 2) w4_tile_kernel(const __grid_constant__ CUtensorMap codes, const W4Tile a) {
+    constexpr int XBLOCK = NX * 128, XHALF = 2 * XBLOCK;       // 64 columns of x, half a slab of it
+    constexpr int XC = NX * 16 / kTileThreads;                 // 16-byte chunks of half a slab of x a thread
+    constexpr int NC = NX / 2, STAGES = TileSmem<NX>::kStages; // columns of D a thread reads
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t done[2], ready[2], full[STAGES];
+    __shared__ uint32_t tmem_at;
+    __shared__ int abort_flag;
+    const W4Params &p = a.p;
+    uint8_t *const sw = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u), *const sx = sw + STAGES * kTileStage;
+    __nv_bfloat16 *const ss = reinterpret_cast<__nv_bfloat16 *>(sx + TileSmem<NX>::kX);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part_of = warp >> 2 & 1;
+    const uint32_t ranks = w4_cluster_size(), rank = w4_cluster_rank();
+    const int64_t n0 = (int64_t)(blockIdx.x / ranks) * kTileRows;
+    const int m0 = blockIdx.y * NX, m = min(p.m - m0, NX);
+    const int first = rank * a.share, last = min(first + a.share, a.slabs);
+    const int row_in = (warp & 3) * 32 + lane;                 // this thread's row of W, and lane of TMEM
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&ready[i], kTileThreads / 32);
+        }
+        for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        __syncwarp();
+        tmem_alloc(&tmem_at, kTileTmem);
+        tmem_relinquish();
+    }
+    auto fetch = [&](int slab) {               // one thread
+        const int s = (slab - first) % STAGES;
+        mbar_arrive_expect_tx(&full[s], kTileStage);
+        tma_load_3d(sw + s * kTileStage, &codes, &full[s], slab * (kSlab / 2), (int)n0, 0);
+    };
+    // x: chunk e of half a slab is columns 8 (e & 15) .. of row e >> 4
+    auto load_x = [&](uint4 (&v)[XC], int at) {
+#pragma unroll
+        for (int i = 0; i < XC; ++i) {
+            const int e = tid + i * kTileThreads, xr = e >> 4, col = at + (e & 15) * 8;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (xr < m && at < last * kSlab && col < p.k)
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(p.x + (int64_t)(m0 + xr) * p.ldx + col));
+        }
+    };
+    // scales of the slabs from `slab` on; zeros past the columns, whose codes TMA fills with zeros (code -8)
+    auto load_scales = [&](int slab) {
+        constexpr int U = 8;                   // loads in flight
+        const int left = last - slab, g0 = slab * kSlab >> p.group_log2;
+        const int per_log2 = 8 + (left > 4 ? 3 : left > 2 ? 2 : left > 1 ? 1 : 0) - p.group_log2;
+        for (int e0 = tid; e0 < kTileRows << per_log2; e0 += U * kTileThreads) {
+            __nv_bfloat16 f[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int e = e0 + i * kTileThreads, r = e >> per_log2, g = g0 + (e & ((1 << per_log2) - 1));
+                f[i] = __float2bfloat16_rn(0.0f);
+                if (r < kTileRows && n0 + r < p.n && g < p.groups) f[i] = p.scales[(n0 + r) * p.groups + g];
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int e = e0 + i * kTileThreads, r = e >> per_log2;
+                if (r < kTileRows) ss[r * kScalePitch + (e & ((1 << per_log2) - 1))] = f[i];
+            }
+        }
+    };
+    uint4 xv[XC];
+    float acc[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
+    if (warp < kTileThreads / 32) {
+        load_x(xv, first * kSlab);
+        if (first < last) load_scales(first);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at, lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const Watchdog wd{a.err, &abort_flag, a.timeout_ns, 12};
+    const int halves = first < last ? 2 * (last - first) : 0;
+    // most waits find their phase complete: a test first (try_wait alone cost 240 cycles)
+    auto wait = [&](uint64_t *bar, int phase, int site) { return mbar_test_wait(bar, phase & 1) || mbar_wait(bar, phase & 1, wd, site); };
+    if (warp == kTileThreads / 32) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, NX);
+            for (int s = first; s < min(first + STAGES, last); ++s) fetch(s);
+            int u = 0;
+            for (; u < halves; ++u) {
+                const int j = u & 1;
+                if (!wait(&ready[j], u >> 1, 3)) break;
+                tc_fence_after();
+                const uint64_t xd = sdesc_sw128(smem_u32(sx) + j * XHALF, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    umma_ts(tmem + kTileD + ((u >> 2) & 1) * NX, tmem + j * 64 + 8 * k, xd + ((k / 4) * XBLOCK + (k % 4) * 32) / 16, idesc,
+                            k > 0 || (u & 3) ? 1u : 0u);
+                umma_commit(&done[j]);
+                // both halves of the slab are widened: its stage is free
+                const int to = first + (u >> 1) + STAGES;
+                if (j == 1 && to < last) fetch(to);
+            }
+            if (u < halves) {
+                // a wait ran out: products and copies in flight must end before TMEM and shared memory go
+                for (int v = max(0, u - 2); v < u; ++v) mbar_drain(&done[v & 1], (v >> 1) & 1, 100000000ull);
+                for (int s = u >> 1; s < min((u >> 1) + STAGES, last - first); ++s)
+                    mbar_drain(&full[s % STAGES], (s / STAGES) & 1, 100000000ull);
+            }
+        }
+        __syncwarp();
+    } else {
+        bool bad = false;
+        // the sums of columns 512 e .. of this CTA's share: the products of four half slabs in one accumulator
+        auto collect = [&](int e) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < NC; c += 16) {
+                float d[16];
+                tmem_ld16f_sync(tmem + lanes + kTileD + (e & 1) * NX + part_of * NC + c, d);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[c + i] += d[i];
+            }
+        };
+        int u = 0, collected = 0;
+        for (; u < halves; ++u) {
+            const int it = u >> 1, j = u & 1, s = it % STAGES;
+            if (j == 0 && it > 0 && it % kScaleSlabs == 0) {
+                named_bar_sync(1, kTileThreads);       // the last scales are read
+                load_scales(first + it);
+                named_bar_sync(1, kTileThreads);
+            }
+            bad = !wait(&full[s], it / STAGES, 1);
+            if (u >= 2) bad |= !wait(&done[j], (u - 2) >> 1, 2);       // buffer j is free
+            if (!__all_sync(0xffffffffu, !bad)) break;
+            if (u > 4 && (u & 3) == 1) collect(collected++);
+            const __nv_bfloat16 *const sr = ss + row_in * kScalePitch;
+            const int col0 = (it % kScaleSlabs) * kSlab + j * 128 + part_of * 64;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const __nv_bfloat16 f = sr[(col0 + q * 32) >> p.group_log2];
+                const uint4 w = *reinterpret_cast<const uint4 *>(sw + s * kTileStage + sw128_offset(row_in, j * 4 + part_of * 2 + q));
+                const __nv_bfloat162 sc = __halves2bfloat162(f, f);
+                uint32_t r[16];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t v[4];
+                    w4_widen(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w, sc, v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) r[4 * i + k] = v[k];
+                }
+                tmem_st16(tmem + lanes + j * 64 + part_of * 32 + q * 16, r);
+            }
+#pragma unroll
+            for (int i = 0; i < XC; ++i) {
+                const int e = tid + i * kTileThreads, xr = e >> 4, c = e & 15;
+                *reinterpret_cast<uint4 *>(sx + j * XHALF + (c >> 3) * XBLOCK + sw128_offset(xr, c & 7)) =
+                    make_uint4(__byte_perm(xv[i].x, xv[i].z, 0x5410), __byte_perm(xv[i].x, xv[i].z, 0x7632),
+                               __byte_perm(xv[i].y, xv[i].w, 0x5410), __byte_perm(xv[i].y, xv[i].w, 0x7632));
+            }
+            fence_proxy_async_smem();
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ready[j]);
+            load_x(xv, first * kSlab + (u + 1) * 128);
+        }
+        if (halves && u == halves) {
+            // the last products, and with them all before
+            if (__all_sync(0xffffffffu, wait(&done[(u - 1) & 1], (u - 1) >> 1, 4)))
+                while (collected <= (u - 1) >> 2) collect(collected++);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTileTmem);
+    }
+    if (ranks == 1) {
+        if (warp < kTileThreads / 32 && n0 + row_in < p.n) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (part_of * NC + i < m) w4_store(p, m0 + part_of * NC + i, n0 + row_in, acc[i]);
+        }
+        return;
+    }
+    // [NX][128] sums in the slab's place; every CTA of the cluster adds up its share of the rows of W
+    float *const part = reinterpret_cast<float *>(sx);
+    if (warp < kTileThreads / 32) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) part[(part_of * NC + i) * kTileRows + row_in] = acc[i];
+    }
+    w4_cluster_sync();
+    const int rows = kTileRows / ranks;
+    for (int e = tid; e < m * rows; e += kTileThreads + 32) {
+        const int xr = e / rows, at = rank * rows + e % rows;
+        if (n0 + at >= p.n) continue;
+        float sum = 0.0f;
+        for (uint32_t r = 0; r < ranks; ++r) sum += w4_load_of(smem_u32(part + xr * kTileRows + at), r);
+        w4_store(p, m0 + xr, n0 + at, sum);
+    }
+    w4_cluster_sync();                         // the others may still read this CTA's sums
+}
+
 // A word of 8 codes a thread: 16 bytes out, whole lines a warp.
 constexpr int kDequantUnroll = 4;
 
@@ -270,12 +552,76 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const __nv_bfloat16 *w
 }
 
 // ------------------------------------------------------------------------------------------------
+// fp32 results of many rows
+// ------------------------------------------------------------------------------------------------
+// The GEMM's sums stay in the tensor core, which truncates them: relative errors of 1.6e-6 at 2048 columns and 7.7e-6 at
+// 8192, far below a bf16 result's rounding but not an fp32 one's.  There it runs on runs of kSumColumns columns, whose
+// results are added up in rounded fp32 (7e-7).
+constexpr int kSumColumns = 1024, kSumParts = 4;
+
+__global__ void __launch_bounds__(256) w4_sum_kernel(const float4 *parts, int32_t n_parts, int64_t part4, int64_t rows, uint32_t row4,
+                                                     float *y, int64_t ldy, uint32_t cols, int32_t add) {
+    const int64_t total = rows * row4, stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
+        const int64_t row = i / row4;
+        const uint32_t col = (uint32_t)(i - row * row4) * 4;
+        float4 v[kSumParts];
+#pragma unroll
+        for (int k = 0; k < kSumParts; ++k)
+            if (k < n_parts) v[k] = parts[k * part4 + i];
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float *out = y + row * ldy + col;
+        if (add)
+            for (int j = 0; j < 4; ++j) s[j] = col + j < cols ? out[j] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kSumParts; ++k)
+            if (k < n_parts) s[0] += v[k].x, s[1] += v[k].y, s[2] += v[k].z, s[3] += v[k].w;
+        for (int j = 0; j < 4; ++j)
+            if (col + j < cols) out[j] = s[j];
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
 // host
 // ------------------------------------------------------------------------------------------------
 
-// Rows of x that go to w4_rows_kernel: the GEMM's 128 x 256 tiles leave most SMs idle below 4096 rows of W (100 rows,
-// 2048 x 2048: 19 us against 13; at 2048 -> 12288 the GEMM's 34 us are half of what four blocks of 32 rows take).
-static bool w4_few(int64_t m, int64_t n_out) { return m <= NOMAS_W4_FEW_ROWS || (m <= 128 && n_out <= 4096); }
+// Runs of columns that an fp32 result of the GEMM is summed in (1: the GEMM writes y itself), pitch of a part's rows.
+static int64_t w4_runs(int64_t k_in, int y_dtype) {
+    return y_dtype == NOMAS_DTYPE_F32 ? (k_in + kSumColumns - 1) / kSumColumns : 1;
+}
+static int64_t w4_part_pitch(int64_t n_out) { return (n_out + 3) / 4 * 4; }
+
+// Bytes of the bf16 weights, at the front of the workspace.
+static size_t w4_weight_bytes(int64_t n_out, int64_t k_in) { return ((size_t)n_out * (size_t)k_in * 2 + 255) / 256 * 256; }
+
+static int enqueue_w4_sums(const void *x, int64_t m, int64_t k_in, int64_t ldx, const void *w, int64_t n_out, float *y, int64_t ldy,
+                           float *parts, int32_t *status, nomas_stream stream) {
+    const int64_t pitch = w4_part_pitch(n_out), runs = w4_runs(k_in, NOMAS_DTYPE_F32);
+    const auto *xb = static_cast<const __nv_bfloat16 *>(x);
+    const auto *wb = static_cast<const __nv_bfloat16 *>(w);
+    for (int64_t r0 = 0; r0 < runs; r0 += kSumParts) {
+        const int n = (int)(runs - r0 < kSumParts ? runs - r0 : kSumParts);
+        for (int i = 0; i < n; ++i) {
+            const int64_t k0 = (r0 + i) * kSumColumns, kc = k_in - k0 < kSumColumns ? k_in - k0 : kSumColumns;
+            const int rc = nomas_linear_bf16(xb + k0, m, kc, ldx, wb + k0, n_out, k_in, parts + i * m * pitch, pitch, NOMAS_DTYPE_F32,
+                                             status, stream);
+            if (rc) return rc;
+        }
+        const int64_t total = m * (pitch / 4), most = (int64_t)sm_count() * 16, ctas = (total + 255) / 256;
+        w4_sum_kernel<<<(unsigned)(ctas < most ? ctas : most), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+            reinterpret_cast<const float4 *>(parts), n, m * (pitch / 4), m, (uint32_t)(pitch / 4), y, ldy, (uint32_t)n_out, r0 > 0);
+        const int rc = check_launch("w4_sum_kernel launch");
+        if (rc) return rc;
+    }
+    return NOMAS_OK;
+}
+
+// Rows of x that need no GEMM: up to 128 of them its 128 x 256 tiles leave most SMs idle below 4096 rows of W, and walk
+// long rows one after the other (us, GEMM against this file's kernels: 128 x 4096 -> 4096 39 / 21, x 8192 -> 8192 84 / 65,
+// x 2048 -> 12288 27 / 36).
+static bool w4_few(int64_t m, int64_t n_out, int64_t k_in) {
+    return m <= NOMAS_W4_FEW_ROWS || (m <= 128 && (n_out <= 4096 || k_in >= 4096));
+}
 
 static int group_log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
 
@@ -326,6 +672,62 @@ static int pick_w4_rows(const W4Params &p, cudaStream_t st) {
     return p.k >= (NT == 1 ? 2048 : 4096) ? launch_w4_rows<NT, 1, 16>(p, st) : launch_w4_rows<NT, 1, 8>(p, st);
 }
 
+// Whether few rows of x go to w4_tile_kernel rather than w4_rows_kernel, which takes 32 of them at a time and has less
+// to set up (us, rows against tiles: 64 x 8192 -> 8192 64 / 32, x 2048 -> 12288 28 / 20, x 4096 -> 4096 19 / 15,
+// x 2048 -> 2048 8 / 11; 30 x 8192 -> 8192 32 / 26, x 2048 -> 12288 14 / 17; 128 x 2048 -> 2048 15 / 12).
+static bool w4_tiles(int64_t m, int64_t n_out, int64_t k_in) {
+    const int64_t weights = n_out * k_in;
+    return m > 64 ? weights >= 1 << 22 : m > 32 ? weights >= 1 << 23 : m > 16 && weights >= 1 << 26;
+}
+
+template <int NX>
+static int launch_w4_tile(const W4Params &p, int32_t *status, cudaStream_t st) {
+    CUtensorMap map;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.k / 2, (cuuint64_t)p.n, 1};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.k / 2, (cuuint64_t)p.k / 2 * (cuuint64_t)p.n};
+    const cuuint32_t box[3] = {kSlab / 2, kTileRows, 1};
+    if (!make_tensor_map_3d(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return NOMAS_ECUDA;
+    W4Tile a{};
+    a.p = p;
+    a.slabs = (p.k + kSlab - 1) / kSlab;
+    a.err = reinterpret_cast<int *>(status);
+    a.timeout_ns = wait_limit_ns();
+    // CTAs of a cluster: the slabs that the busiest SM gets, two CTAs of it a fifth faster than one after the other, and
+    // 1.7 slabs' time for each doubling of the cluster
+    const int64_t blocks = (p.m + NX - 1) / NX, tiles = (p.n + kTileRows - 1) / kTileRows;
+    int ranks = 1;
+    int64_t least = INT64_MAX;
+    for (int r = 1, step = 0; r <= 8 && r <= a.slabs; r *= 2, ++step) {
+        const int64_t ctas = (tiles * blocks * r + sm_count() - 1) / sm_count(), share = (a.slabs + r - 1) / r;
+        const int64_t cost = ctas * share * (ctas == 1 ? 10 : 8) + 17 * step;
+        if (cost < least) least = cost, ranks = r;
+    }
+    a.share = (a.slabs + ranks - 1) / ranks;
+    auto kernel = w4_tile_kernel<NX>;
+    static std::atomic<uint64_t> allowed{0};   // devices on which the kernel may use its shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !(allowed.load() >> dev & 1))) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<NX>::kBytes);
+        if (e == cudaSuccess && dev < 64) allowed.fetch_or((uint64_t)1 << dev);
+    }
+    if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(w4 smem)", (int)e, cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * ranks), (unsigned)blocks);
+    cfg.blockDim = dim3(kTileThreads + 32);
+    cfg.dynamicSmemBytes = TileSmem<NX>::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, map, a);
+    return e == cudaSuccess ? NOMAS_OK : cuda_fail("w4_tile_kernel launch", (int)e, cudaGetErrorString(e));
+}
+
 }  // namespace nomas
 
 using namespace nomas;
@@ -355,9 +757,11 @@ extern "C" int nomas_w4_dequant(const uint8_t *codes, const void *scales, int gr
     return enqueue_w4_dequant(codes, scales, group, n_out, k_in, w, reinterpret_cast<cudaStream_t>(stream));
 }
 
-extern "C" size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in) {
-    if (n_out < 1 || k_in < 1 || w4_few(m, n_out)) return 0;
-    return (size_t)n_out * (size_t)k_in * 2;
+extern "C" size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in, int y_dtype) {
+    if (m < 1 || n_out < 1 || k_in < 1 || w4_few(m, n_out, k_in)) return 0;
+    const int64_t runs = w4_runs(k_in, y_dtype);
+    const int64_t parts = runs == 1 ? 0 : runs < kSumParts ? runs : kSumParts;
+    return w4_weight_bytes(n_out, k_in) + (size_t)parts * (size_t)m * (size_t)w4_part_pitch(n_out) * sizeof(float);
 }
 
 extern "C" int nomas_w4a16_linear(const void *x, int64_t m, int64_t k_in, int64_t ldx, const uint8_t *codes,
@@ -369,15 +773,19 @@ extern "C" int nomas_w4a16_linear(const void *x, int64_t m, int64_t k_in, int64_
     if (ldx < k_in || ldx % 8 != 0 || ldy < n_out) return NOMAS_EINVAL;
     if (y_dtype != NOMAS_DTYPE_F32 && y_dtype != NOMAS_DTYPE_BF16) return NOMAS_EINVAL;
     if (m >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
-    if (!w4_few(m, n_out) && (!workspace || !aligned16(workspace))) return NOMAS_EINVAL;
+    if (!w4_few(m, n_out, k_in) && (!workspace || !aligned16(workspace))) return NOMAS_EINVAL;
     if (m == 0) return NOMAS_OK;
     DeviceScope dev(codes);
     if (dev.rc) return dev.rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (!w4_few(m, n_out)) {
+    if (!w4_few(m, n_out, k_in)) {
         rc = enqueue_w4_dequant(codes, scales, group, n_out, k_in, workspace, st);
         if (rc) return rc;
-        return nomas_linear_bf16(x, m, k_in, ldx, workspace, n_out, k_in, y, ldy, y_dtype, status, stream);
+        if (w4_runs(k_in, y_dtype) == 1)
+            return nomas_linear_bf16(x, m, k_in, ldx, workspace, n_out, k_in, y, ldy, y_dtype, status, stream);
+        return enqueue_w4_sums(x, m, k_in, ldx, workspace, n_out, static_cast<float *>(y), ldy,
+                               reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w4_weight_bytes(n_out, k_in)), status,
+                               stream);
     }
     W4Params p{};
     p.codes = codes;
@@ -389,6 +797,8 @@ extern "C" int nomas_w4a16_linear(const void *x, int64_t m, int64_t k_in, int64_
     p.groups = (int32_t)((k_in + group - 1) / group);
     p.group_log2 = group_log2_of(group);
     p.y_bf16 = y_dtype == NOMAS_DTYPE_BF16;
+    if (w4_tiles(m, n_out, k_in))
+        return m <= 32 ? launch_w4_tile<32>(p, status, st) : launch_w4_tile<64>(p, status, st);
     if (m <= 8) return pick_w4_rows<1>(p, st);
     if (m <= 16) return pick_w4_rows<2>(p, st);
     return pick_w4_rows<4>(p, st);

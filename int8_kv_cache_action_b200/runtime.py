@@ -379,8 +379,8 @@ class Int4Linear:
         if m:
             ws = 0
             if m > N.NOMAS_W4_FEW_ROWS:
-                keep = torch.empty(N.nomas_w4a16_workspace_bytes(m, self.n_out, self.k_in), dtype=torch.uint8,
-                                   device=x.device)
+                keep = torch.empty(N.nomas_w4a16_workspace_bytes(m, self.n_out, self.k_in, _DTYPES[out.dtype]),
+                                   dtype=torch.uint8, device=x.device)
                 ws = keep.data_ptr()
             N._check(N.lib.nomas_w4a16_linear(x.data_ptr(), m, self.k_in, _pitch(x), self._codes, self._scales, self.group,
                                               self.n_out, out.data_ptr(), _pitch(out), _DTYPES[out.dtype], ws,

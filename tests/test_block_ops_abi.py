@@ -63,6 +63,8 @@ def test_w4_refusals(N):
         assert call(**kw) == N.NOMAS_EINVAL, kw
     assert N.nomas_w4a16_workspace_bytes(1, 4096, 4096) == 0
     assert N.nomas_w4a16_workspace_bytes(1000, 4096, 2048) == 4096 * 2048 * 2
+    assert N.nomas_w4a16_workspace_bytes(1000, 4095, 2048, N.NOMAS_DTYPE_F32) == 4095 * 2048 * 2 + 2 * 1000 * 4096 * 4
+    assert N.nomas_w4a16_workspace_bytes(1000, 4096, 1024, N.NOMAS_DTYPE_F32) == 4096 * 1024 * 2
     assert N.nomas_w4_quantize(0, 16, 64, 64, 64, A, A) == N.NOMAS_EINVAL
     assert N.nomas_w4_quantize(A, 16, 64, 63, 64, A, A) == N.NOMAS_EINVAL
     assert N.nomas_w4_dequant(A, A, 64, 16, 64, A + 8) == N.NOMAS_EINVAL

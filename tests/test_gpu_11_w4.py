@@ -94,6 +94,48 @@ def test_large(m, n, k, group):
     _check(lin(x, out_dtype=F32), x, lin)
 
 
+# tcgen05 tiles: clusters of 1 to 8, ragged rows and columns, a long row whose scales come in parts, idle ranks
+@pytest.mark.parametrize("m,n,k,group", [(33, 4100, 2080, 64), (64, 1000, 8416, 32), (100, 4096, 4128, 128), (20, 16500, 4128, 32),
+                                         (40, 130, 65568, 64), (128, 2048, 2304, 64), (47, 20000, 448, 128)])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+def test_tiles(m, n, k, group, out_dtype):
+    x = _acts(m, k, 16).cuda()
+    lin = _codes(n, k, group, 17)
+    y = lin(x, out_dtype=out_dtype)
+    assert lin.status() == N.NOMAS_OK
+    _check(y, x, lin)
+    assert torch.equal(lin(x, out_dtype=out_dtype), y)
+
+
+@pytest.mark.parametrize("m", [5, 40, 100, 300])
+@pytest.mark.parametrize("n,k", [(520, 2080), (2050, 8192)])
+def test_fp32_results_keep_fp32_precision(m, n, k):
+    # runs of at most 1024 columns in the tensor core, truncated: each run's 65 sums lose under 65 2^-23 of the run's largest
+    # partial sum, about sqrt(1024 / k) of the result's size, and the rounded sums of the runs far less
+    x, lin = _acts(m, k, 20).cuda(), _codes(n, k, 64, 21)
+    y = lin(x, out_dtype=F32).double()
+    ref = x.double() @ lin.dequantized().double().t()
+    assert float((y - ref).norm() / ref.norm()) <= 65 * 2.0 ** -23
+    edge = torch.full((m, n + 3), 5.0, device="cuda")
+    lin(x, out=edge[:, :n])
+    assert torch.equal(edge[:, :n].double(), y) and torch.all(edge[:, n:] == 5.0)
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    x = _acts(64, 4096, 18).cuda()
+    lin = _codes(4096, 4096, 64, 19)
+    ref = lin(x)
+    prev = N.nomas_set_wait_limit_ns(0)
+    try:
+        lin(x)
+        torch.cuda.synchronize()
+        status = lin.status()
+    finally:
+        N.nomas_set_wait_limit_ns(prev)
+    assert status == N.NOMAS_ETIMEOUT
+    assert torch.equal(lin(x), ref) and lin.status() == N.NOMAS_OK
+
+
 def test_each_weight_reaches_its_place():
     # x = rows of the identity: y is the dequantised weights themselves, exactly
     k = 256
