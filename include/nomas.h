@@ -418,6 +418,8 @@ typedef struct {
  *   positions  fp32 [tokens][3] (device): time, height, width of each token; exactly one
  *              of grid and positions is given.  A non-finite position gives NaN in its axis' channels.
  *   dtype      NOMAS_DTYPE_BF16 or NOMAS_DTYPE_F32, of every x and y
+ * Positions, origins and steps times a pair's turns must stay finite in fp64; a grid's far indices keep full
+ * precision, a given position that of its fp32.
  * tokens = 0 does nothing.  Runs on the device that holds the first tensor.  Errors: NOMAS_EINVAL for a
  * bad pointer, stride, spec or grid; NOMAS_EUNSUPPORTED for 2^31 tokens or more. */
 int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *grid, const float *positions, int64_t tokens,
@@ -442,16 +444,17 @@ int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *grid, const f
 #define NOMAS_NORM_MAX_COLS 16384
 
 /* w, b nullable (y = xhat without w and b, unit_offset then without effect); mean, rstd fp32 [rows], nullable.
- * y may be x when the types and pitches agree. */
+ * y may be x when the types and pitches agree; other overlaps are not allowed. */
 int nomas_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int64_t ldx, int x_dtype, const void *w,
                         const void *b, int64_t ldp, int p_dtype, int64_t rows_per_group, int unit_offset, float eps,
                         void *y, int64_t ldy, int y_dtype, float *mean, float *rstd, nomas_stream stream);
 
-/* Bytes of the backward pass' workspace: 0 on invalid arguments, else at least 16. */
+/* Bytes of the backward pass' workspace on the current device: 0 on invalid arguments, else at least 16. */
 size_t nomas_layernorm_workspace_bytes(int64_t rows, int64_t cols, int64_t rows_per_group);
 
 /* mean, rstd: of the forward call.  dx, dw, db: each nullable, not all; dw, db fp32 [groups][cols], pitch
- * ldg.  dx may be dy or x when types and pitches agree.  workspace: device buffer, 16-byte aligned, read
+ * ldg.  dx may be dy or x when types and pitches agree (other overlaps are
+ * not allowed).  workspace: device buffer, 16-byte aligned, read
  * and written by this call alone (calls that share it must not overlap); NULL allowed without dw and db. */
 int nomas_layernorm_bwd(const void *dy, int64_t lddy, int y_dtype, const void *x, int64_t ldx, int x_dtype,
                         int64_t rows, int64_t cols, const void *w, int64_t ldp, int p_dtype, int64_t rows_per_group,

@@ -49,7 +49,8 @@ DeviceScope::DeviceScope(const void *p) : rc(NOMAS_OK), previous(-1) {
         rc = cuda_fail("cudaPointerGetAttributes", (int)e, cudaGetErrorString(e));
         return;
     }
-    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) {
+    if (at.type == cudaMemoryTypeManaged) return;       // any device's: the current one
+    if (at.type != cudaMemoryTypeDevice) {
         rc = NOMAS_EINVAL;
         return;
     }

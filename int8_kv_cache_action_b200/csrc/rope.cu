@@ -418,6 +418,8 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
         long double at = 1.0L / 6.283185307179586476925286766559L;
         for (int i = 0; i < spec->axis_dim[a] / 2; ++i, ++pair, at *= root) {
             const double turns = (double)at;
+            if (!std::isfinite(turns) || (grid && (!std::isfinite(turns * grid->origin[a]) || !std::isfinite(turns * grid->step[a]))))
+                return NOMAS_EINVAL;
             if (grid)
                 p.pair[pair] = RopePair{rope_fraction(turns * grid->origin[a]), rope_fraction(turns * grid->step[a])};
             else

@@ -332,7 +332,6 @@ class Int4Linear:
             raise ValueError("scales: contiguous bfloat16 [N, ceil(K / group)] on the device of codes")
         self.codes, self.scales, self.group = codes, scales, group
         self.status_word = torch.zeros(4, dtype=torch.int32, device=codes.device)
-        self._codes, self._scales, self._status = codes.data_ptr(), scales.data_ptr(), self.status_word.data_ptr()
 
     @classmethod
     def from_weights(cls, w: torch.Tensor, group: int = 64, stream=None) -> "Int4Linear":
@@ -369,22 +368,22 @@ class Int4Linear:
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.k_in or x.stride(1) != 1:
             raise ValueError("x: bf16 [M, K] with contiguous rows")
         m = x.shape[0]
+        _same_device(self.codes, x, out)
+        if (out_dtype if out is None else out.dtype) not in _DTYPES:
+            raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
         if out is None:
             out = x.new_empty((m, self.n_out), dtype=out_dtype)
         elif out.shape != (m, self.n_out) or out.stride(1) != 1:
             raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
-        if out.dtype not in _DTYPES:
-            raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
-        _same_device(self.codes, x, out)
         if m:
             ws = 0
             if m > N.NOMAS_W4_FEW_ROWS:
                 keep = torch.empty(N.nomas_w4a16_workspace_bytes(m, self.n_out, self.k_in, _DTYPES[out.dtype]),
                                    dtype=torch.uint8, device=x.device)
                 ws = keep.data_ptr()
-            N._check(N.lib.nomas_w4a16_linear(x.data_ptr(), m, self.k_in, _pitch(x), self._codes, self._scales, self.group,
-                                              self.n_out, out.data_ptr(), _pitch(out), _DTYPES[out.dtype], ws,
-                                              self._status, st), "nomas_w4a16_linear")
+            N._check(N.lib.nomas_w4a16_linear(x.data_ptr(), m, self.k_in, _pitch(x), self.codes.data_ptr(), self.scales.data_ptr(),
+                                              self.group, self.n_out, out.data_ptr(), _pitch(out), _DTYPES[out.dtype], ws,
+                                              self.status_word.data_ptr(), st), "nomas_w4a16_linear")
         return out
 
     def status(self, stream=None) -> int:
@@ -392,7 +391,7 @@ class Int4Linear:
         if st is None:
             with _on(self.codes, stream):
                 return self.status()
-        return N.nomas_status_read(self._status, st)
+        return N.nomas_status_read(self.status_word.data_ptr(), st)
 
 
 # ------------------------------------------------------------------------------------------------
@@ -513,13 +512,13 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
             return layer_norm(x, weight, bias, eps, rows_per_group, unit_offset, out_dtype, out, want_stats)
     pitch, p_dtype, _ = _norm_params(x, weight, bias, rows_per_group)
     rows, cols = x.shape
+    _same_device(x, weight, bias, out)
+    if ((out_dtype or x.dtype) if out is None else out.dtype) not in _DTYPES:
+        raise ValueError("out: bf16 or fp32 [rows, C] with contiguous rows")
     if out is None:
         out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or out.stride(1) != 1:
         raise ValueError("out: bf16 or fp32 [rows, C] with contiguous rows")
-    if out.dtype not in _DTYPES:
-        raise ValueError("out: bf16 or fp32 [rows, C] with contiguous rows")
-    _same_device(x, weight, bias, out)
     mean = rstd = None
     if want_stats:
         mean = x.new_empty(rows, dtype=torch.float32)

@@ -33,6 +33,7 @@ def test_rope_refusals(N):
     for t in (dict(x=0), dict(y=0), dict(x=A + 8), dict(heads=0), dict(xt=260), dict(xh=-8), dict(y=A + 16, yh=64), dict(y=A + 16, yt=0),
               dict(yt=512)):                                    # the last: in place with other strides
         assert call(tensor=t) == N.NOMAS_EINVAL, t
+    assert call(spec=(128, (2, 2, 64), 1e-300), grid=N.make_rope_grid(2, 2, (0, 0, 1e300))) == N.NOMAS_EINVAL
     assert call(tokens=1 << 31) == N.NOMAS_EUNSUPPORTED
 
 
