@@ -455,7 +455,8 @@ size_t nomas_layernorm_workspace_bytes(int64_t rows, int64_t cols, int64_t rows_
 /* mean, rstd: of the forward call.  dx, dw, db: each nullable, not all; dw, db fp32 [groups][cols], pitch
  * ldg.  dx may be dy or x when types and pitches agree (other overlaps are
  * not allowed).  workspace: device buffer, 16-byte aligned, read
- * and written by this call alone (calls that share it must not overlap); NULL allowed without dw and db. */
+ * and written by this call alone (calls that share it must not overlap); NULL allowed without dw and db, and when
+ * nomas_layernorm_workspace_bytes gives 16. */
 int nomas_layernorm_bwd(const void *dy, int64_t lddy, int y_dtype, const void *x, int64_t ldx, int x_dtype,
                         int64_t rows, int64_t cols, const void *w, int64_t ldp, int p_dtype, int64_t rows_per_group,
                         int unit_offset, const float *mean, const float *rstd, void *dx, int64_t lddx, float *dw,

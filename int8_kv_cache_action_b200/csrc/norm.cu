@@ -874,11 +874,12 @@ static int any_fwd(NormParams &p, bool wide, cudaStream_t st) {
 // Shares of the backward pass: the CTAs that the device holds at once (`per_sm` on an SM), each with at least a round
 // of rows.
 static void bwd_shares(int64_t rows, int64_t cols, int per_sm, int64_t *share, int64_t *ctas) {
-    const int64_t most = per_sm * (int64_t)sm_count(), least = cols <= 512 ? 16 : 4;
+    // small ones: a single share needs no second launch
+    const int64_t most = per_sm * (int64_t)sm_count(), least = rows * cols <= 32768 ? rows : cols <= 512 ? 16 : 4;
     int64_t s = (rows + most - 1) / most;
     if (s < least) s = least;
-    *share = s;
-    *ctas = (rows + s - 1) / s;
+    *share = s < 1 ? 1 : s;
+    *ctas = (rows + *share - 1) / *share;
 }
 
 template <typename TX, typename TY, int CH, int NV, int R, int T, bool ALONE>
@@ -992,7 +993,8 @@ extern "C" int nomas_layernorm_bwd(const void *dy, int64_t lddy, int y_dtype, co
     if ((dw && !matrix_ok(dw, cols, ldg, NOMAS_DTYPE_F32)) || (db && !matrix_ok(db, cols, ldg, NOMAS_DTYPE_F32)))
         return NOMAS_EINVAL;
     if (dx && ((dx == x && lddx != ldx) || (dx == dy && (lddx != lddy || x_dtype != y_dtype)))) return NOMAS_EINVAL;
-    if ((dw || db) && (!workspace || !aligned16(workspace))) return NOMAS_EINVAL;
+    if ((dw || db) && (workspace ? !aligned16(workspace) : nomas_layernorm_workspace_bytes(rows, cols, rows_per_group) > 16))
+        return NOMAS_EINVAL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     DeviceScope dev(x);
     if (dev.rc) return dev.rc;

@@ -620,7 +620,9 @@ static int enqueue_w4_sums(const void *x, int64_t m, int64_t k_in, int64_t ldx, 
 // long rows one after the other (us, GEMM against this file's kernels: 128 x 4096 -> 4096 39 / 21, x 8192 -> 8192 84 / 65,
 // x 2048 -> 12288 27 / 36).
 static bool w4_few(int64_t m, int64_t n_out, int64_t k_in) {
-    return m <= NOMAS_W4_FEW_ROWS || (m <= 128 && (n_out <= 4096 || k_in >= 4096));
+    if (m <= NOMAS_W4_FEW_ROWS || (m <= 128 && (n_out <= 4096 || k_in >= 4096))) return true;
+    // products that take less than the GEMM's launches (some 20 us)
+    return m <= 4096 && m * n_out * k_in <= (int64_t)1 << 29;
 }
 
 static int group_log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }

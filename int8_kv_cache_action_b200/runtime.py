@@ -31,6 +31,9 @@ def _bf16_strides(t: torch.Tensor) -> Tuple[int, int]:
 _DTYPES = {torch.float32: N.NOMAS_DTYPE_F32, torch.bfloat16: N.NOMAS_DTYPE_BF16}
 
 
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _ptr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -69,12 +72,12 @@ class _on:
 
 def _stream_on(ref: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> Optional[int]:
     """The current stream of `ref`'s device as an address, or None when a call needs _on first."""
-    if not ref.is_cuda:
-        raise ValueError(f"expected a CUDA tensor, got one on {ref.device}")
     index = ref.get_device()
-    if stream is not None or index != torch.cuda.current_device():
+    if index < 0 or not ref.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {ref.device}")
+    if stream is not None or index != _current_device():
         return None
-    return torch._C._cuda_getCurrentRawStream(index)
+    return _raw_stream(index)
 
 
 def segment_text(n_frames: int, head_len: int, tails: Sequence[Tuple[int, int, int]] = ()):
@@ -365,25 +368,30 @@ class Int4Linear:
         if st is None:
             with _on(self.codes, stream):
                 return self(x, out_dtype, out)
-        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.k_in or x.stride(1) != 1:
+        codes, n, k, shape, strides = self.codes, self.n_out, self.k_in, x.shape, x.stride()
+        if x.dtype is not torch.bfloat16 or len(shape) != 2 or shape[1] != k or strides[1] != 1:
             raise ValueError("x: bf16 [M, K] with contiguous rows")
-        m = x.shape[0]
-        _same_device(self.codes, x, out)
-        if (out_dtype if out is None else out.dtype) not in _DTYPES:
+        m = shape[0]
+        _same_device(codes, x, out)
+        dtype = _DTYPES.get(out_dtype if out is None else out.dtype)
+        if dtype is None or (out is not None and (out.shape != (m, n) or out.stride(1) != 1)):
             raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
         if out is None:
-            out = x.new_empty((m, self.n_out), dtype=out_dtype)
-        elif out.shape != (m, self.n_out) or out.stride(1) != 1:
-            raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
+            out, ldy = x.new_empty((m, n), dtype=out_dtype), n
+        else:
+            ldy = _pitch(out)
         if m:
             ws = 0
             if m > N.NOMAS_W4_FEW_ROWS:
-                keep = torch.empty(N.nomas_w4a16_workspace_bytes(m, self.n_out, self.k_in, _DTYPES[out.dtype]),
-                                   dtype=torch.uint8, device=x.device)
-                ws = keep.data_ptr()
-            N._check(N.lib.nomas_w4a16_linear(x.data_ptr(), m, self.k_in, _pitch(x), self.codes.data_ptr(), self.scales.data_ptr(),
-                                              self.group, self.n_out, out.data_ptr(), _pitch(out), _DTYPES[out.dtype], ws,
-                                              self.status_word.data_ptr(), st), "nomas_w4a16_linear")
+                need = N.nomas_w4a16_workspace_bytes(m, n, k, dtype)
+                if need:
+                    keep = x.new_empty(need, dtype=torch.uint8)
+                    ws = keep.data_ptr()
+            # a single row's own stride says nothing
+            rc = N.lib.nomas_w4a16_linear(x.data_ptr(), m, k, strides[0] if m > 1 else k, codes.data_ptr(), self.scales.data_ptr(),
+                                          self.group, n, out.data_ptr(), ldy, dtype, ws, self.status_word.data_ptr(), st)
+            if rc:
+                N._check(rc, "nomas_w4a16_linear")
         return out
 
     def status(self, stream=None) -> int:
@@ -482,6 +490,8 @@ def _norm_params(x, weight, bias, rows_per_group):
     rows, cols = x.shape
     if rows_per_group < 0:
         raise ValueError("rows_per_group: at least 0")
+    if weight is None and bias is None:
+        return cols, N.NOMAS_DTYPE_F32, -(-rows // rows_per_group) if rows_per_group else 1
     groups = -(-rows // rows_per_group) if rows_per_group else 1
     pitch, dtype = 0, None
     for p in (weight, bias):

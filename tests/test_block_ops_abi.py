@@ -47,7 +47,7 @@ def test_layernorm_refusals(N):
     for kw in (dict(x=0), dict(y=0), dict(x=A + 1), dict(xt=2), dict(yt=-1), dict(pt=7), dict(rows=-1), dict(cols=0), dict(ldx=63), dict(ldy=63),
                dict(ldp=63), dict(w=A + 1), dict(rpg=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(y=A, yt=0), dict(y=A, ldy=72)):
         assert f(**kw) == N.NOMAS_EINVAL, kw
-    for kw in (dict(dy=0), dict(x=0), dict(mean=0), dict(rstd=0), dict(dx=0, dw=0, db=0), dict(lddx=63), dict(ldg=63), dict(ws=0),
+    for kw in (dict(dy=0), dict(x=0), dict(mean=0), dict(rstd=0), dict(dx=0, dw=0, db=0), dict(lddx=63), dict(ldg=63), dict(rows=4096, ws=0),
                dict(ws=A + 8), dict(dw=A + 2), dict(rpg=-1), dict(lddy=63), dict(dx=A, lddx=72), dict(dx=A, yt=0)):
         assert g(**kw) == N.NOMAS_EINVAL, kw
     assert f(cols=N.NOMAS_NORM_MAX_COLS + 1) == N.NOMAS_EUNSUPPORTED and g(rows=1 << 31) == N.NOMAS_EUNSUPPORTED
@@ -60,7 +60,7 @@ def test_w4_refusals(N):
     assert call(m=0) == N.NOMAS_OK
     for kw in (dict(x=0), dict(x=A + 2), dict(m=-1), dict(k=48, ldx=48), dict(k=0), dict(ldx=56), dict(ldx=68), dict(codes=0), dict(codes=A + 8),
                dict(scales=0), dict(scales=A + 2), dict(group=16), dict(group=96), dict(n=0), dict(y=0), dict(ldy=15), dict(yt=2), dict(st=0),
-               dict(m=1000), dict(m=1000, ws=A + 4)):
+               dict(m=1000, n=1 << 16, ldy=1 << 16), dict(m=1000, n=1 << 16, ldy=1 << 16, ws=A + 4)):
         assert call(**kw) == N.NOMAS_EINVAL, kw
     assert N.nomas_w4a16_workspace_bytes(1, 4096, 4096) == 0
     assert N.nomas_w4a16_workspace_bytes(1000, 4096, 2048) == 4096 * 2048 * 2
