@@ -501,7 +501,7 @@ const char *nomas_status_string(int status);
 const char *nomas_last_error(void);
 
 /* Test and diagnostic hook: the limit, in nanoseconds, of every bounded wait inside the attention
- * and append kernels, the sparse selection's pooling kernel and the linear layer (process-wide, default
+ * and append kernels, the sparse selection's pooling kernel and the linear layers (process-wide, default
  * 2 000 000 000 = 2 s; it applies to later calls).  A
  * wait that runs out records NOMAS_ETIMEOUT in the cache's device error word, and every role of the
  * CTA then leaves its loop, lets its in-flight copies and MMAs complete and releases TMEM, so the
