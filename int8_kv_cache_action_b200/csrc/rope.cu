@@ -18,8 +18,10 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeTable = 4096;               // (cos, sin) entries of a CTA's tokens: 32 KB
 constexpr int kRopeMaxPairs = NOMAS_ROPE_MAX_HEAD_DIM / 2;
 
-// How a pair's values are reached: in one 16-byte chunk (interleaved), in two that the same thread holds (halves,
-// where every axis' half is whole chunks), or one by one (halves of other widths: rope_pairs_kernel).
+// How a pair's values are reached: in one 16-byte chunk (interleaved), in two chunks that the same thread holds (halves,
+// where every axis' half is whole chunks of 16, or in bf16 of 8 bytes), or one by one (halves of other widths:
+// rope_pairs_kernel).  26400 tokens of 2 x 16 x 128 in bf16, halves: chunks of 16 bytes (axes 32, 48, 48) 83 us, of 8
+// (16, 56, 56) 76, one by one (44, 42, 42) 111, which is also what 16, 56, 56 took one by one.
 enum RopeForm { kRopeInside = 0, kRopeTwoChunks = 1, kRopePairs = 2 };
 
 struct RopeTensor {
@@ -51,10 +53,19 @@ struct RopeParams {
     int32_t pairs, all_pairs;                  // pairs that turn, head_dim / 2
 };
 
-template <typename T>
-struct Chunk {
-    static constexpr int V = 16 / sizeof(T);
+// V values of T in one access.
+template <int BYTES>
+struct ChunkOf;
+template <>
+struct ChunkOf<16> {
+    typedef uint4 type;
 };
+template <>
+struct ChunkOf<8> {
+    typedef uint2 type;
+};
+template <typename T, int V>
+using Chunk = typename ChunkOf<V * (int)sizeof(T)>::type;
 
 __device__ __forceinline__ void unpack(const uint4 &c, float (&v)[8]) {
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -67,17 +78,25 @@ __device__ __forceinline__ void unpack(const uint4 &c, float (&v)[8]) {
 __device__ __forceinline__ void unpack(const uint4 &c, float (&v)[4]) {
     v[0] = __uint_as_float(c.x), v[1] = __uint_as_float(c.y), v[2] = __uint_as_float(c.z), v[3] = __uint_as_float(c.w);
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+__device__ __forceinline__ void unpack(const uint2 &c, float (&v)[4]) {
+    v[0] = __uint_as_float(c.x << 16), v[1] = __uint_as_float(c.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(c.y << 16), v[3] = __uint_as_float(c.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void pack(const float (&v)[8], uint4 &c) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t *>(&b);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    c = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[4]) {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+__device__ __forceinline__ void pack(const float (&v)[4], uint4 &c) {
+    c = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ void pack(const float (&v)[4], uint2 &c) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    c = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
 // The rotated chunk with the words behind its first `turned` channels as they were: channels that no axis
@@ -95,9 +114,8 @@ __device__ __forceinline__ uint4 keep_behind(uint4 out, const uint4 &in, int tur
 // First channel of item j in the two-chunk form, and how far its second chunk is: item j holds pairs
 // j V .. j V + V - 1, whose axis starts at channel axis_at[a] = 2 x (pairs in front of it).  Behind the axes
 // the item is two neighbouring chunks that pass through.
-template <typename T>
+template <uint32_t V>
 __device__ __forceinline__ void rope_two(const RopeParams &p, uint32_t j, uint32_t &c, uint32_t &apart) {
-    constexpr uint32_t V = Chunk<T>::V;
     const uint32_t ch = 2 * V * j;
     apart = V;
     c = ch;
@@ -143,9 +161,10 @@ __device__ __forceinline__ void turn(float &a, float &b, const float2 &cs) {
 
 // NS items of a token per thread: one while a token has no more items than the CTA threads (then `abreast` tokens side
 // by side), else two, 256 apart, of the 512 that blockIdx.y names.
-template <typename T, int FORM, int NS>
+template <typename T, int V, int FORM, int NS>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int V = Chunk<T>::V, U = 4 / NS;          // tokens in flight
+    typedef Chunk<T, V> C;
+    constexpr int U = 4 / NS;                  // tokens in flight
     __shared__ __align__(16) float2 table[kRopeTable];
     __shared__ RopePair pairs[kRopeMaxPairs];
     for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) pairs[i] = p.pair[i];
@@ -169,7 +188,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
         const RopeTensor &t = p.t[k];
         const uint32_t in = it - t.first_item, head = fdiv(in, p.per_head), j = in - head * p.per_head.d;
         uint32_t c = j * V, gap = 0;
-        if constexpr (FORM == kRopeTwoChunks) rope_two<T>(p, j, c, gap);
+        if constexpr (FORM == kRopeTwoChunks) rope_two<V>(p, j, c, gap);
         apart[s] = gap * sizeof(T);
         pair0[s] = j * (FORM == kRopeTwoChunks ? V : V / 2);
         const int64_t tok = (int64_t)token0 + side;
@@ -179,14 +198,14 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
         y_step[s] = t.y_tok * p.abreast;
     }
     for (uint32_t at = 0; at < n; at += U * p.abreast) {
-        uint4 v0[U][NS], v1[FORM == kRopeTwoChunks ? U : 1][NS];
+        C v0[U][NS], v1[FORM == kRopeTwoChunks ? U : 1][NS];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
                 if (live[s] && at + u * p.abreast + side < n) {
-                    v0[u][s] = *reinterpret_cast<const uint4 *>(x[s]);
-                    if constexpr (FORM == kRopeTwoChunks) v1[u][s] = *reinterpret_cast<const uint4 *>(x[s] + apart[s]);
+                    v0[u][s] = *reinterpret_cast<const C *>(x[s]);
+                    if constexpr (FORM == kRopeTwoChunks) v1[u][s] = *reinterpret_cast<const C *>(x[s] + apart[s]);
                 }
                 x[s] += x_step[s];
             }
@@ -211,25 +230,27 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
                         if (pair0[s] + V / 2 <= p.pairs) {
 #pragma unroll
                             for (int i = 0; i < V / 2; ++i) turn(a[2 * i], a[2 * i + 1], cs[i]);
-                            v0[u][s] = pack(a);
+                            pack(a, v0[u][s]);
                         } else {               // the axes end in this chunk, or before it
 #pragma unroll
                             for (int i = 0; i < V / 2; ++i)
                                 if (pair0[s] + i < p.pairs) turn(a[2 * i], a[2 * i + 1], cs[i]);
-                            v0[u][s] = keep_behind<V>(pack(a), v0[u][s], 2 * (p.pairs - pair0[s]));
+                            const C in = v0[u][s];
+                            pack(a, v0[u][s]);
+                            v0[u][s] = keep_behind<V>(v0[u][s], in, 2 * (p.pairs - pair0[s]));
                         }
-                        *reinterpret_cast<uint4 *>(y[s]) = v0[u][s];
+                        *reinterpret_cast<C *>(y[s]) = v0[u][s];
                     } else {
                         if (pair0[s] < p.pairs) {      // whole items turn or pass
                             float b[V];
                             unpack(v1[u][s], b);
 #pragma unroll
                             for (int i = 0; i < V; ++i) turn(a[i], b[i], cs[i]);
-                            v0[u][s] = pack(a);
-                            v1[u][s] = pack(b);
+                            pack(a, v0[u][s]);
+                            pack(b, v1[u][s]);
                         }
-                        *reinterpret_cast<uint4 *>(y[s]) = v0[u][s];
-                        *reinterpret_cast<uint4 *>(y[s] + apart[s]) = v1[u][s];
+                        *reinterpret_cast<C *>(y[s]) = v0[u][s];
+                        *reinterpret_cast<C *>(y[s] + apart[s]) = v1[u][s];
                     }
                 }
                 y[s] += y_step[s];
@@ -326,16 +347,12 @@ static int launch_rope_pairs(unsigned grid, const RopeParams &p, cudaStream_t st
     return check_launch("rope_pairs_kernel launch");
 }
 
-template <typename T>
-static int launch_rope(RopeForm form, dim3 grid, unsigned threads, const RopeParams &p, cudaStream_t st) {
-    const bool two = p.items.d > kRopeThreads;
-    if (form == kRopeInside) {
-        if (two) rope_kernel<T, kRopeInside, 2><<<grid, threads, 0, st>>>(p);
-        else rope_kernel<T, kRopeInside, 1><<<grid, threads, 0, st>>>(p);
-    } else {
-        if (two) rope_kernel<T, kRopeTwoChunks, 2><<<grid, threads, 0, st>>>(p);
-        else rope_kernel<T, kRopeTwoChunks, 1><<<grid, threads, 0, st>>>(p);
-    }
+template <typename T, int V, int FORM>
+static int launch_rope(dim3 grid, unsigned threads, const RopeParams &p, cudaStream_t st) {
+    if (p.items.d > kRopeThreads)
+        rope_kernel<T, V, FORM, 2><<<grid, threads, 0, st>>>(p);
+    else
+        rope_kernel<T, V, FORM, 1><<<grid, threads, 0, st>>>(p);
     return check_launch("rope_kernel launch");
 }
 
@@ -381,16 +398,18 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
     }
     if (tokens >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
 
-    const int esize = dtype == NOMAS_DTYPE_BF16 ? 2 : 4, v = 16 / esize;
+    const int esize = dtype == NOMAS_DTYPE_BF16 ? 2 : 4;
+    int v = 16 / esize;                        // values of a chunk
     p.axis_at[0] = 0;
     for (int a = 0; a < 3; ++a) p.axis_at[a + 1] = p.axis_at[a] + spec->axis_dim[a];
     p.pairs = p.axis_at[3] / 2;
     p.all_pairs = spec->head_dim / 2;
     RopeForm form = kRopeInside;
     if (spec->pairing == NOMAS_ROPE_HALVES) {
-        form = spec->head_dim % (2 * v) == 0 ? kRopeTwoChunks : kRopePairs;
-        for (int a = 0; a < 3; ++a)
-            if (spec->axis_dim[a] % (2 * v) != 0) form = kRopePairs;
+        int all = spec->head_dim;
+        for (int a = 0; a < 3; ++a) all |= spec->axis_dim[a];
+        if (all % (2 * v) != 0) v = 4;         // chunks of 8 bytes in bf16
+        form = all % (2 * v) == 0 ? kRopeTwoChunks : kRopePairs;
     }
     const int64_t per_head = spec->head_dim / (form == kRopeTwoChunks ? 2 * v : v);
     int64_t items = 0;
@@ -463,6 +482,10 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
     if (per_cta < p.abreast) per_cta = p.abreast <= kRopeTable / p.all_pairs ? p.abreast : kRopeTable / p.all_pairs;
     p.tokens_per_cta = (uint32_t)per_cta;
     const dim3 grid_dim((unsigned)((tokens + per_cta - 1) / per_cta), (unsigned)parts);
-    return dtype == NOMAS_DTYPE_BF16 ? launch_rope<__nv_bfloat16>(form, grid_dim, threads, p, st)
-                                     : launch_rope<float>(form, grid_dim, threads, p, st);
+    if (dtype == NOMAS_DTYPE_F32)
+        return form == kRopeInside ? launch_rope<float, 4, kRopeInside>(grid_dim, threads, p, st)
+                                   : launch_rope<float, 4, kRopeTwoChunks>(grid_dim, threads, p, st);
+    if (form == kRopeInside) return launch_rope<__nv_bfloat16, 8, kRopeInside>(grid_dim, threads, p, st);
+    return v == 8 ? launch_rope<__nv_bfloat16, 8, kRopeTwoChunks>(grid_dim, threads, p, st)
+                  : launch_rope<__nv_bfloat16, 4, kRopeTwoChunks>(grid_dim, threads, p, st);
 }

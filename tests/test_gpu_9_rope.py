@@ -76,7 +76,8 @@ def test_inverse_is_the_gradient_and_in_place_is_the_same(axes, pairing):
     assert abs(float(lhs - rhs)) <= bound
 
 
-@pytest.mark.parametrize("pairing,axes", [("interleaved", (16, 56, 56)), ("halves", (32, 48, 32)), ("halves", (22, 20, 22))])
+@pytest.mark.parametrize("pairing,axes", [("interleaved", (16, 56, 56)), ("halves", (32, 48, 32)), ("halves", (16, 40, 56)),
+                                          ("halves", (22, 20, 22))])
 def test_views_and_untouched_neighbours(pairing, axes):
     t, h, d = 77, 3, 128
     qkv = _randn((t, 3, h, d), BF16, 7).cuda()                # fused projection: q and k are views
@@ -95,18 +96,20 @@ def test_views_and_untouched_neighbours(pairing, axes):
     _check(y, shared, pos, axes, pairing)
 
 
-@pytest.mark.parametrize("pairing", ["interleaved", "halves"])
-def test_channels_that_pass_through_keep_every_bit_and_nan_stays_in_its_axis(pairing):
+@pytest.mark.parametrize("pairing,axes", [("interleaved", (8, 16, 16)), ("interleaved", (6, 14, 18)), ("halves", (16, 16, 16)),
+                                          ("halves", (8, 16, 16)), ("halves", (6, 14, 18))])
+def test_channels_that_pass_through_keep_every_bit_and_nan_stays_in_its_axis(pairing, axes):
+    a, b, c = axes[0], axes[0] + axes[1], sum(axes)
     x = _randn((3, 2, 64), BF16, 8).cuda()
-    x[..., 40:] = float("inf")
-    x[1, 0, 41] = float("nan")
-    x[0, 1, 42] = -0.0
+    x[..., c:] = float("inf")
+    x[1, 0, c + 1] = float("nan")
+    x[0, 1, c + 2] = -0.0
     pos = torch.tensor([[1.0, float("nan"), 2.0], [0.0, 1.0, 3.0], [4.0, 5.0, float("inf")]], device="cuda")
-    y = AxisRope(64, (8, 16, 16), pairing=pairing)(x, positions=pos)
-    assert torch.equal(y[..., 40:].view(torch.int16), x[..., 40:].view(torch.int16))
+    y = AxisRope(64, axes, pairing=pairing)(x, positions=pos)
+    assert torch.equal(y[..., c:].view(torch.int16), x[..., c:].view(torch.int16))
     nan = torch.isnan(y.float()).any(1).cpu()
-    assert nan[0, 8:24].all() and not nan[0, :8].any() and not nan[0, 24:40].any()
-    assert nan[2, 24:40].all() and not nan[2, :24].any() and not nan[1, :40].any()
+    assert nan[0, a:b].all() and not nan[0, :a].any() and not nan[0, b:c].any()
+    assert nan[2, b:c].all() and not nan[2, :b].any() and not nan[1, :c].any()
 
 
 def test_offsets_past_32_bits():
