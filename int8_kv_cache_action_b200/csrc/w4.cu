@@ -452,6 +452,13 @@ __global__ void __launch_bounds__(kTileThreads + 32, 2) w4_tile_kernel(const __g
             if (lane == 0) mbar_arrive(&ready[j]);
             load_x(xv, first * kSlab + (u + 1) * 128);
         }
+        // a warp whose wait ran out still meets the others at the barriers ahead: they may have waited in time
+        if (u < halves)
+            for (int it = (u >> 1) + 1; it < last - first; ++it)
+                if (it % kScaleSlabs == 0) {
+                    named_bar_sync(1, kTileThreads);
+                    named_bar_sync(1, kTileThreads);
+                }
         if (halves && u == halves) {
             // the last products, and with them all before
             if (__all_sync(0xffffffffu, wait(&done[(u - 1) & 1], (u - 1) >> 1, 4)))

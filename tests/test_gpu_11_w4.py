@@ -121,9 +121,10 @@ def test_fp32_results_keep_fp32_precision(m, n, k):
     assert torch.equal(edge[:, :n].double(), y) and torch.all(edge[:, n:] == 5.0)
 
 
-def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
-    x = _acts(64, 4096, 18).cuda()
-    lin = _codes(4096, 4096, 64, 19)
+@pytest.mark.parametrize("n,k", [(4096, 4096), (2048, 32768)])          # one and two loads of a CTA's scales
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(n, k):
+    x = _acts(64, k, 18).cuda()
+    lin = _codes(n, k, 64, 19)
     ref = lin(x)
     prev = N.nomas_set_wait_limit_ns(0)
     try:
