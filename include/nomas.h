@@ -403,8 +403,9 @@ typedef struct {
 } nomas_rope_grid;
 
 /* One tensor of a call: [tokens][heads][head_dim], strides in elements, multiples of 8 (0 allowed for x: a
- * value that several tokens or heads share).  y may be x with the same strides (in place); otherwise x and
- * y, and the tensors of one call, must not overlap. */
+ * value that several tokens or heads share; of y, heads lie inside a token's stride or tokens inside a
+ * head's).  y may be x with the same strides (in place); otherwise x and y, and the tensors of one call,
+ * must not overlap (inputs may). */
 typedef struct {
     const void *x;
     void *y;
@@ -453,10 +454,9 @@ int nomas_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int64_t ldx, 
 size_t nomas_layernorm_workspace_bytes(int64_t rows, int64_t cols, int64_t rows_per_group);
 
 /* mean, rstd: of the forward call.  dx, dw, db: each nullable, not all; dw, db fp32 [groups][cols], pitch
- * ldg.  dx may be dy or x when types and pitches agree (other overlaps are
- * not allowed).  workspace: device buffer, 16-byte aligned, read
- * and written by this call alone (calls that share it must not overlap); NULL allowed without dw and db, and when
- * nomas_layernorm_workspace_bytes gives 16. */
+ * ldg.  dx may be dy or x when types and pitches agree (other overlaps are not allowed).  workspace: device
+ * buffer, 16-byte aligned, read and written by this call alone (calls that share it must not overlap); NULL
+ * allowed without dw and db, and when nomas_layernorm_workspace_bytes gives 16. */
 int nomas_layernorm_bwd(const void *dy, int64_t lddy, int y_dtype, const void *x, int64_t ldx, int x_dtype,
                         int64_t rows, int64_t cols, const void *w, int64_t ldp, int p_dtype, int64_t rows_per_group,
                         int unit_offset, const float *mean, const float *rstd, void *dx, int64_t lddx, float *dw,
@@ -478,10 +478,11 @@ int nomas_w4_quantize(const void *w, int64_t n_out, int64_t k_in, int64_t ldw, i
 /* Dequantise into bf16 weights w [N][K] (dense). */
 int nomas_w4_dequant(const uint8_t *codes, const void *scales, int group, int64_t n_out, int64_t k_in, void *w,
                      nomas_stream stream);
-/* Bytes of the workspace of a nomas_w4a16_linear call with m rows and results of y_dtype: 0 for few rows (the
- * weights are widened in registers: up to NOMAS_W4_FEW_ROWS rows always), else the transient bf16 weights of the
- * tensor-core GEMM (N * K * 2 bytes, rounded up to 256) and, for fp32 results of more than 1024 columns, up to four
- * partial results: the tensor core truncates its sums, so runs of 1024 columns are added up in rounded fp32. */
+/* Bytes of the workspace of a nomas_w4a16_linear call with m rows and results of y_dtype: 0 for sizes that the
+ * call refuses and for few rows (the weights are widened on chip: up to NOMAS_W4_FEW_ROWS rows always), else the
+ * transient bf16 weights of the tensor-core GEMM (N * K * 2 bytes, rounded up to 256) and, for fp32 results of more
+ * than 1024 columns, up to four partial results: the tensor core truncates its sums, so runs of 1024 columns are added
+ * up in rounded fp32. */
 #define NOMAS_W4_FEW_ROWS 64
 size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in, int y_dtype);
 /* y [M][N] = x [M][K] W^T.  workspace may be NULL when nomas_w4a16_workspace_bytes gives 0; status as for

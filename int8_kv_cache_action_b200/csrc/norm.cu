@@ -4,7 +4,8 @@
 // Both directions are bound by HBM: the forward pass reads x and writes y, the backward pass reads dy and
 // x and writes dx, about 8 and 14 flops a value.  A row stays in the registers of a team of threads (a
 // power of two), so that the variance is a second sum over registers (exact differences, no sum of squares
-// that cancels) and memory is read once.
+// that cancels) and memory is read once.  26400 x 2048 in bf16, modulated by groups of 880 rows: forward 40 us,
+// backward 60 us, both 5.4 TB/s, where a copy of this pattern reaches 5.5 to 5.8.
 //   layernorm_row_kernel   forward, one row per team, loads straight into registers: few rows (latency), and
 //                          groups of few rows
 //   layernorm_fwd_kernel   forward, a CTA takes a contiguous share of the rows.  Every thread keeps its own
@@ -13,8 +14,9 @@
 //                          copies of 8 bytes hold the next rows in registers.  A thread owns
 //                          columns, whose weight and bias stay in its registers for a group, and takes R rows
 //                          at a time, which share the two exchanges of sums between the warps.
-//   layernorm_bwd_kernel   the same for dy and x; dw and db of a group add up in the registers in row order.  Groups inside a share are written at once; where a group
-//                          goes on in the next share, its sums so far go to the workspace (two slots a CTA).
+//   layernorm_bwd_kernel   the same for dy and x; dw and db of a group add up in the registers in row order.  Groups
+//                          inside a share are written at once; where a group goes on in the next share, its sums so
+//                          far go to the workspace (two slots a CTA).
 //   layernorm_grad_kernel  adds up the shares of such groups, in share order.
 #include <atomic>
 
@@ -494,8 +496,9 @@ __device__ __forceinline__ void flush_grads(const NormBwdParams &p, Pair (&sum_w
     }
 }
 
-// Backward ring: stages of R rows of x and dy, up to three (eight of single rows) in about 200 KB; without two (rows above 8192 columns
-// in fp32), and in narrow layouts (no copies of 8 bytes and more), rows are loaded straight into registers.
+// Backward ring: stages of R rows of x and dy, up to three (eight of single rows) in about 200 KB; without two (rows
+// above 8192 columns in fp32), and in narrow layouts (no copies of 8 bytes and more), rows are loaded straight into
+// registers.
 template <typename TX, typename TY, int CH, int NV, int R, int T>
 struct BwdRing {
     static constexpr int kStage = R * NV * CH * (int)(sizeof(TX) + sizeof(TY)) * T;

@@ -634,12 +634,16 @@ static bool w4_few(int64_t m, int64_t n_out, int64_t k_in) {
 
 static int group_log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
 
-static int check_w4(const void *codes, const void *scales, int group, int64_t n_out, int64_t k_in) {
-    if (!codes || !scales || !aligned16(codes) || !aligned16(scales) || group_log2_of(group) < 0) return NOMAS_EINVAL;
+static int check_w4_sizes(int64_t n_out, int64_t k_in) {
     if (n_out < 1 || k_in < 32 || k_in % 32 != 0) return NOMAS_EINVAL;
     // 32-bit offsets: of 32 rows in w4_rows_kernel, of words in w4_dequant_kernel
     if (n_out >= (int64_t)1 << 31 || k_in >= (int64_t)1 << 26 || n_out * (k_in / 8) >= (int64_t)1 << 31) return NOMAS_EUNSUPPORTED;
     return NOMAS_OK;
+}
+
+static int check_w4(const void *codes, const void *scales, int group, int64_t n_out, int64_t k_in) {
+    if (!codes || !scales || !aligned16(codes) || !aligned16(scales) || group_log2_of(group) < 0) return NOMAS_EINVAL;
+    return check_w4_sizes(n_out, k_in);
 }
 
 static int enqueue_w4_dequant(const uint8_t *codes, const void *scales, int group, int64_t n_out, int64_t k_in, void *w,
@@ -767,7 +771,7 @@ extern "C" int nomas_w4_dequant(const uint8_t *codes, const void *scales, int gr
 }
 
 extern "C" size_t nomas_w4a16_workspace_bytes(int64_t m, int64_t n_out, int64_t k_in, int y_dtype) {
-    if (m < 1 || n_out < 1 || k_in < 1 || w4_few(m, n_out, k_in)) return 0;
+    if (m < 1 || m >= (int64_t)1 << 31 || check_w4_sizes(n_out, k_in) || w4_few(m, n_out, k_in)) return 0;
     const int64_t runs = w4_runs(k_in, y_dtype);
     const int64_t parts = runs == 1 ? 0 : runs < kSumParts ? runs : kSumParts;
     return w4_weight_bytes(n_out, k_in) + (size_t)parts * (size_t)m * (size_t)w4_part_pitch(n_out) * sizeof(float);

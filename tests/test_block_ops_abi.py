@@ -31,8 +31,16 @@ def test_rope_refusals(N):
                dict(grid=N.make_rope_grid(2, 2, (float("nan"), 0, 0))), dict(grid=N.make_rope_grid(2, 2, step=(1, float("inf"), 1)))):
         assert call(**kw) == N.NOMAS_EINVAL, kw
     for t in (dict(x=0), dict(y=0), dict(x=A + 8), dict(heads=0), dict(xt=260), dict(xh=-8), dict(y=A + 16, yh=64), dict(y=A + 16, yt=0),
-              dict(yt=512)):                                    # the last: in place with other strides
+              dict(y=A + 16, yt=128, yh=192),                   # y's tokens and heads meet
+              dict(yt=512)):                                    # in place with other strides
         assert call(tensor=t) == N.NOMAS_EINVAL, t
+    assert call(n=2) == N.NOMAS_EINVAL                           # two results in one place
+    assert call(n=2, tensor=dict(y=A + 16)) == N.NOMAS_EINVAL
+    spec, grid = N.make_rope_spec(128, (16, 56, 56)), N.make_rope_grid(2, 2)
+    first = (A, A + 16, 256, 128, 256, 128, 2)
+    for x, y in ((A + 16, A + 32), (A + 32, A)):                # the second reads the first one's result, writes what it reads
+        pair = N.make_rope_tensors([first, (x, y, 256, 128, 256, 128, 2)])
+        assert N.nomas_rope(spec, grid, 0, 4, pair, 2, N.NOMAS_DTYPE_BF16, 0) == N.NOMAS_EINVAL
     assert call(spec=(128, (2, 2, 64), 1e-300), grid=N.make_rope_grid(2, 2, (0, 0, 1e300))) == N.NOMAS_EINVAL
     assert call(tokens=1 << 31) == N.NOMAS_EUNSUPPORTED
 
@@ -66,6 +74,8 @@ def test_w4_refusals(N):
     assert N.nomas_w4a16_workspace_bytes(1000, 4096, 2048) == 4096 * 2048 * 2
     assert N.nomas_w4a16_workspace_bytes(1000, 4095, 2048, N.NOMAS_DTYPE_F32) == 4095 * 2048 * 2 + 2 * 1000 * 4096 * 4
     assert N.nomas_w4a16_workspace_bytes(1000, 4096, 1024, N.NOMAS_DTYPE_F32) == 4096 * 1024 * 2
+    for size in ((0, 4096, 2048), (1000, 0, 2048), (1000, 4096, 2040), (1000, 1 << 31, 64), (1 << 31, 4096, 2048)):
+        assert N.nomas_w4a16_workspace_bytes(*size) == 0
     assert N.nomas_w4_quantize(0, 16, 64, 64, 64, A, A) == N.NOMAS_EINVAL
     assert N.nomas_w4_quantize(A, 16, 64, 63, 64, A, A) == N.NOMAS_EINVAL
     assert N.nomas_w4_dequant(A, A, 64, 16, 64, A + 8) == N.NOMAS_EINVAL
