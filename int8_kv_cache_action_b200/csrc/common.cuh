@@ -60,6 +60,15 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// One lane of a converged warp, always the same one.  Products issued under it by a warp whose operands are uniform follow
+// each other as the tensor core takes them; issued under lane == 0 one of the GEMM's took about 150 cycles whatever its
+// width.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Shared state of a CTA's watchdog: once any wait runs out, every later wait of the
 // CTA returns at once so that all roles reach the common exit.
 struct Watchdog {

@@ -7,14 +7,14 @@
 //   w8_quantize_kernel   one CTA per weight row: absmax, s = RN(absmax / 127), codes
 //   w8_dequant_kernel    bf16(RN(code * s)), 16 weights per thread (HBM-bound)
 //   gemm2_bf16_kernel    y = x W^T on the tensor cores (more than 128 rows): persistent clusters of two
-//                        CTAs on an SM pair, tiles of 256 x 256 computed by tcgen05.mma.cta_group::2
-//                        M256 N256 K16 from the even CTA; each CTA stages 128 rows of A and 128 rows
-//                        of B per K step of 64 through a six-stage TMA ring (16 + 16 KB, 128-byte
-//                        swizzle, no multicast) and holds its 128 accumulator rows in TMEM (two
-//                        256-column accumulators, so the epilogue of a tile overlaps the main loop of
+//                        CTAs on an SM pair, tiles of 256 x 256 (or 224, 192) computed by
+//                        tcgen05.mma.cta_group::2 M256 K16 from the even CTA; each CTA stages 128 rows of A
+//                        and half of the tile's rows of B per K step of 64 through a six-stage TMA ring
+//                        (16 + 16 KB, 128-byte swizzle, no multicast) and holds its 128 accumulator rows
+//                        in TMEM (two accumulators, so the epilogue of a tile overlaps the main loop of
 //                        the next); four epilogue warps per CTA read them with tcgen05.ld.
-//   gemm_bf16_kernel     the same on one SM per 128 x 256 tile (four-stage ring of 16 + 32 KB, SS
-//                        tcgen05.mma M128 N256 K16), for at most 128 rows.
+//   gemm_bf16_kernel     the same on one SM per 128 x 256 (or 128) tile (SS tcgen05.mma M128 K16), for at
+//                        most 128 rows.
 #include <cstdio>
 #include <mutex>
 
@@ -86,16 +86,19 @@ __global__ void w8_dequant_tail_kernel(const int8_t *codes, const float *scales,
 // bf16 GEMM on the tensor cores
 // ------------------------------------------------------------------------------------------------
 
-constexpr int kGemmBM = 128, kGemmBN = 256, kGemmBK = 64, kGemmStages = 4;
+constexpr int kGemmBM = 128, kGemmBK = 64;
+constexpr int kGemmD = 256;                 // TMEM columns of an accumulator, of two
 constexpr int kGemmThreads = 192;           // warp 0 TMA, warp 1 MMA + TMEM owner, warps 2-5 epilogue
 
+template <int BN>
 struct GemmCfg {
     static constexpr int A_STAGE = kGemmBM * kGemmBK * 2;          // 16 KB
-    static constexpr int B_STAGE = kGemmBN * kGemmBK * 2;          // 32 KB
+    static constexpr int B_STAGE = BN * kGemmBK * 2;
     static constexpr int STAGE = A_STAGE + B_STAGE;
-    static constexpr int OFF_BAR = kGemmStages * STAGE;
-    // full, empty [kGemmStages]; acc_full, acc_empty [2]; mma_done
-    static constexpr int NBAR = 2 * kGemmStages + 5;
+    static constexpr int STAGES = 192 * 1024 / STAGE;
+    static constexpr int OFF_BAR = STAGES * STAGE;
+    // full, empty [STAGES]; acc_full, acc_empty [2]; mma_done
+    static constexpr int NBAR = 2 * STAGES + 5;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int BYTES = OFF_MISC + 32;
     static constexpr int SMEM = BYTES + 1024;                      // slack for 1024-byte alignment
@@ -104,7 +107,7 @@ struct GemmCfg {
 struct GemmParams {
     int64_t M, N;
     int32_t k_iters;                        // ceil(K / 64)
-    int32_t n_nblk;                         // ceil(N / 256)
+    int32_t n_nblk;                         // ceil(N / columns of a tile)
     int64_t n_tiles;
     void *y;
     int64_t ldy;
@@ -153,22 +156,23 @@ __device__ __forceinline__ void gemm_tile(const GemmParams &p, int64_t t, int &m
     nb = (int)(t - (int64_t)mb * p.n_nblk);
 }
 
+template <int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_bf16_kernel(const __grid_constant__ CUtensorMap ta,
                                                                      const __grid_constant__ CUtensorMap tb,
                                                                      const GemmParams p) {
-    using C = GemmCfg;
+    using C = GemmCfg<BN>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *sm = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
-    uint64_t *full = bars, *empty = bars + kGemmStages;
-    uint64_t *acc_full = empty + kGemmStages, *acc_empty = acc_full + 2, *mma_done = acc_empty + 2;
+    uint64_t *full = bars, *empty = bars + C::STAGES;
+    uint64_t *acc_full = empty + C::STAGES, *acc_empty = acc_full + 2, *mma_done = acc_empty + 2;
     uint32_t *misc = reinterpret_cast<uint32_t *>(sm + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kGemmStages; ++i) {
+        for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
@@ -202,54 +206,59 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_bf16_kernel(const __grid
                 int mb, nb;
                 gemm_tile(p, t, mb, nb);
                 for (int kb = 0; kb < p.k_iters; ++kb) {
-                    if (!(ok = mbar_wait(&empty[s], ph ^ 1, wd, 1))) break;
+                    if (!(ok = (mbar_test_wait(&empty[s], ph ^ 1) || mbar_wait(&empty[s], ph ^ 1, wd, 1)))) break;
                     uint8_t *a = sm + s * C::STAGE;
                     mbar_arrive_expect_tx(&full[s], C::STAGE);
                     tma_load_3d(a, &ta, &full[s], kb * kGemmBK, mb * kGemmBM, 0);
-                    tma_load_3d(a + C::A_STAGE, &tb, &full[s], kb * kGemmBK, nb * kGemmBN, 0);
+                    tma_load_3d(a + C::A_STAGE, &tb, &full[s], kb * kGemmBK, nb * BN, 0);
                     issued |= 1u << s;
                     par = (par & ~(1u << s)) | ((uint32_t)ph << s);
-                    if (++s == kGemmStages) {
+                    if (++s == C::STAGES) {
                         s = 0;
                         ph ^= 1;
                     }
                 }
             }
             // copies in flight must land before the CTA's shared memory is released (abort path)
-            for (int i = 0; i < kGemmStages; ++i)
+            for (int i = 0; i < C::STAGES; ++i)
                 if ((issued >> i) & 1u) mbar_drain(&full[i], (par >> i) & 1u, 100000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------------------------------------ MMA issuer
-            constexpr uint32_t idesc = idesc_bf16_f32(kGemmBM, kGemmBN);
-            const uint64_t d0 = sdesc_sw128(smem_u32(sm), 16, 1024);   // + byte offset / 16 per stage, K step
-            int s = 0, ph = 0, acc = 0;
-            bool ok = true;
-            for (int64_t t = blockIdx.x; ok && t < p.n_tiles; t += gridDim.x, ++acc) {
-                const int buf = acc & 1;
-                if (!(ok = mbar_wait(&acc_empty[buf], ((acc >> 1) & 1) ^ 1, wd, 2))) break;
+        // ---------------------------------------------------------------- MMA issuer
+        constexpr uint32_t idesc = idesc_bf16_f32(kGemmBM, BN);
+        const uint64_t d0 = sdesc_sw128(smem_u32(sm), 16, 1024);       // + byte offset / 16 per stage, K step
+        const uint32_t d_tmem = __shfl_sync(0xffffffffu, tmem, 0);
+        int s = 0, ph = 0, acc = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; ok && t < p.n_tiles; t += gridDim.x, ++acc) {
+            const int buf = acc & 1;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((acc >> 1) & 1) ^ 1, wd, 2)))) break;
+            tc_fence_after();
+            const uint32_t d = d_tmem + (uint32_t)(buf * kGemmD);
+            for (int kb = 0; kb < p.k_iters; ++kb) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_test_wait(&full[s], ph) || mbar_wait(&full[s], ph, wd, 3)))) break;
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(buf * kGemmBN);
-                for (int kb = 0; kb < p.k_iters; ++kb) {
-                    if (!(ok = mbar_wait(&full[s], ph, wd, 3))) break;
-                    tc_fence_after();
-                    const uint64_t da = d0 + (uint64_t)((s * C::STAGE) >> 4);
-                    const uint64_t db = da + (uint64_t)(C::A_STAGE >> 4);
+                const uint64_t da = d0 + (uint64_t)((s * C::STAGE) >> 4);
+                const uint64_t db = da + (uint64_t)(C::A_STAGE >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kGemmBK / 16; ++kk)
                         umma_ss(d, da + (uint64_t)(kk * 2), db + (uint64_t)(kk * 2), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
                     umma_commit(&empty[s]);      // the stage is free once these MMAs have read it
-                    if (++s == kGemmStages) {
-                        s = 0;
-                        ph ^= 1;
-                    }
                 }
-                if (!ok) break;
-                umma_commit(&acc_full[buf]);
+                __syncwarp();
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
-            // every MMA must be complete before TMEM is released, also on the abort path
+            if (!ok) break;
+            if (elect_one()) umma_commit(&acc_full[buf]);
+            __syncwarp();
+        }
+        // every MMA must be complete before TMEM is released, also on the abort path
+        if (elect_one()) {
             umma_commit(mma_done);
             mbar_drain(mma_done, 0, 100000000ull);
         }
@@ -267,11 +276,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_bf16_kernel(const __grid
             gemm_tile(p, t, mb, nb);
             const int64_t row = (int64_t)mb * kGemmBM + g * 32 + lane;
             const bool row_ok = row < p.M;
-            const int64_t col0 = (int64_t)nb * kGemmBN;
+            const int64_t col0 = (int64_t)nb * BN;
 #pragma unroll 1
-            for (int c0 = 0; c0 < kGemmBN; c0 += 32) {
+            for (int c0 = 0; c0 < BN; c0 += 32) {
                 uint32_t r[32];
-                tmem_ld32_sync(tmem + lane_base + (uint32_t)(buf * kGemmBN + c0), r);
+                tmem_ld32_sync(tmem + lane_base + (uint32_t)(buf * kGemmD + c0), r);
                 const int64_t col = col0 + c0;
                 if (!row_ok || col >= p.N) continue;
                 store_row32(p, r, row, col);
@@ -293,25 +302,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_bf16_kernel(const __grid
 // ------------------------------------------------------------------------------------------------
 // bf16 GEMM on SM pairs (cta_group::2)
 // ------------------------------------------------------------------------------------------------
-// A cluster of two CTAs on an SM pair computes a 256 x 256 tile: each CTA stages 128 rows of A and 128
-// rows (output columns) of B per K step, and one tcgen05.mma.cta_group::2 of M256 N256 K16, issued by
+// A cluster of two CTAs on an SM pair computes a 256 x BN tile: each CTA stages 128 rows of A and BN / 2
+// rows (output columns) of B per K step, and one tcgen05.mma.cta_group::2 of M256 N = BN K16, issued by
 // the even CTA, reads both CTAs' halves and accumulates rows 0..127 in the even CTA's TMEM and rows
-// 128..255 in the odd one's.  Per SM this moves 32 KB of operands per K step of 64 instead of the
-// 48 KB of the one-SM 128 x 256 tile for the same MMA work.
+// 128..255 in the odd one's.  With BN = 256 this moves 32 KB of operands per SM and K step of 64 instead of
+// the 48 KB of the one-SM 128 x 256 tile for the same MMA work.
 //   full[s]      even CTA only: one arrive_expect_tx of both CTAs' bytes; both CTAs' copies complete on it
 //   empty[s]     each CTA: the even CTA's MMA commit, multicast to both, frees the stage
 //   acc_full[b]  each CTA: the MMA commit of a tile, multicast to both
 //   acc_empty[b] even CTA only: the four epilogue warps of both CTAs arrive (eight)
-constexpr int kG2Stages = 6;
 constexpr uint16_t kPairMask = 0x3;
 
+template <int BN>
 struct Gemm2Cfg {
     static constexpr int A_STAGE = 128 * kGemmBK * 2;              // 16 KB: this CTA's 128 rows of A
-    static constexpr int B_STAGE = 128 * kGemmBK * 2;              // 16 KB: this CTA's 128 rows of B
+    static constexpr int B_STAGE = BN / 2 * kGemmBK * 2;           // this CTA's half of the tile's rows of B
     static constexpr int STAGE = A_STAGE + B_STAGE;
-    static constexpr int OFF_BAR = kG2Stages * STAGE;
-    // full, empty [kG2Stages]; acc_full, acc_empty [2]; mma_done
-    static constexpr int NBAR = 2 * kG2Stages + 5;
+    static constexpr int STAGES = 192 * 1024 / STAGE;
+    static constexpr int OFF_BAR = STAGES * STAGE;
+    // full, empty [STAGES]; acc_full, acc_empty [2]; mma_done
+    static constexpr int NBAR = 2 * STAGES + 5;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int BYTES = OFF_MISC + 32;
     static constexpr int SMEM = BYTES + 1024;
@@ -372,22 +382,23 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Tile t of a pair's persistent schedule: 256 x 256, N blocks fastest.
+// Tile t of a pair's persistent schedule: 256 x BN, N blocks fastest.
 __device__ __forceinline__ void gemm2_tile(const GemmParams &p, int64_t t, int &mb, int &nb) {
     mb = (int)(t / p.n_nblk);
     nb = (int)(t - (int64_t)mb * p.n_nblk);
 }
 
+template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm2_bf16_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                       const GemmParams p) {
-    using C = Gemm2Cfg;
+    using C = Gemm2Cfg<BN>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *sm = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
-    uint64_t *full = bars, *empty = bars + kG2Stages;
-    uint64_t *acc_full = empty + kG2Stages, *acc_empty = acc_full + 2, *mma_done = acc_empty + 2;
+    uint64_t *full = bars, *empty = bars + C::STAGES;
+    uint64_t *acc_full = empty + C::STAGES, *acc_empty = acc_full + 2, *mma_done = acc_empty + 2;
     uint32_t *misc = reinterpret_cast<uint32_t *>(sm + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -396,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const int64_t pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kG2Stages; ++i) {
+        for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
@@ -430,15 +441,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 int mb, nb;
                 gemm2_tile(p, t, mb, nb);
                 for (int kb = 0; kb < p.k_iters; ++kb) {
-                    if (!(ok = mbar_wait(&empty[s], ph ^ 1, wd, 1))) break;
+                    if (!(ok = (mbar_test_wait(&empty[s], ph ^ 1) || mbar_wait(&empty[s], ph ^ 1, wd, 1)))) break;
                     uint8_t *a = sm + s * C::STAGE;
                     if (even) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
                     const uint32_t fb = even_cta_addr(&full[s]);
                     tma_load_3d_pair(a, &ta, fb, kb * kGemmBK, mb * 256 + (int)rank * 128, 0);
-                    tma_load_3d_pair(a + C::A_STAGE, &tb, fb, kb * kGemmBK, nb * 256 + (int)rank * 128, 0);
+                    tma_load_3d_pair(a + C::A_STAGE, &tb, fb, kb * kGemmBK, nb * BN + (int)rank * (BN / 2), 0);
                     issued |= 1u << s;
                     par = (par & ~(1u << s)) | ((uint32_t)ph << s);
-                    if (++s == kG2Stages) {
+                    if (++s == C::STAGES) {
                         s = 0;
                         ph ^= 1;
                     }
@@ -447,43 +458,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             // the even CTA's full barriers count both CTAs' bytes: it drains them before the final
             // cluster barrier, which the odd CTA passes only after (abort path)
             if (even)
-                for (int i = 0; i < kG2Stages; ++i)
+                for (int i = 0; i < C::STAGES; ++i)
                     if ((issued >> i) & 1u) mbar_drain(&full[i], (par >> i) & 1u, 100000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (even && lane == 0) {
+        if (even) {
             // ------------------------------------------------------------ MMA issuer (even CTA)
-            constexpr uint32_t idesc = idesc_bf16_f32(256, kGemmBN);
+            constexpr uint32_t idesc = idesc_bf16_f32(256, BN);
             const uint64_t d0 = sdesc_sw128(smem_u32(sm), 16, 1024);
+            const uint32_t d_tmem = __shfl_sync(0xffffffffu, tmem, 0);
             int s = 0, ph = 0, acc = 0;
             bool ok = true;
             for (int64_t t = pair; ok && t < p.n_tiles; t += n_pairs, ++acc) {
                 const int buf = acc & 1;
-                if (!(ok = mbar_wait(&acc_empty[buf], ((acc >> 1) & 1) ^ 1, wd, 2))) break;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((acc >> 1) & 1) ^ 1, wd, 2)))) break;
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(buf * kGemmBN);
+                const uint32_t d = d_tmem + (uint32_t)(buf * kGemmD);
                 for (int kb = 0; kb < p.k_iters; ++kb) {
-                    if (!(ok = mbar_wait(&full[s], ph, wd, 3))) break;
+                    if (!(ok = __all_sync(0xffffffffu, mbar_test_wait(&full[s], ph) || mbar_wait(&full[s], ph, wd, 3)))) break;
                     tc_fence_after();
                     const uint64_t da = d0 + (uint64_t)((s * C::STAGE) >> 4);
                     const uint64_t db = da + (uint64_t)(C::A_STAGE >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kGemmBK / 16; ++kk)
-                        umma_ss_pair(d, da + (uint64_t)(kk * 2), db + (uint64_t)(kk * 2), idesc,
-                                     (kb > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit_pair(&empty[s]);
-                    if (++s == kG2Stages) {
+                        for (int kk = 0; kk < kGemmBK / 16; ++kk)
+                            umma_ss_pair(d, da + (uint64_t)(kk * 2), db + (uint64_t)(kk * 2), idesc,
+                                         (kb > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit_pair(&empty[s]);
+                    }
+                    __syncwarp();
+                    if (++s == C::STAGES) {
                         s = 0;
                         ph ^= 1;
                     }
                 }
                 if (!ok) break;
-                umma_commit_pair(&acc_full[buf]);
+                if (elect_one()) umma_commit_pair(&acc_full[buf]);
+                __syncwarp();
             }
             // every MMA must be complete before either CTA releases TMEM or shared memory
-            umma_commit_pair(mma_done);
-            mbar_drain(mma_done, 0, 100000000ull);
+            if (elect_one()) {
+                umma_commit_pair(mma_done);
+                mbar_drain(mma_done, 0, 100000000ull);
+            }
         }
         __syncwarp();
     } else {
@@ -499,11 +517,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             gemm2_tile(p, t, mb, nb);
             const int64_t row = (int64_t)mb * 256 + (int64_t)rank * 128 + g * 32 + lane;
             const bool row_ok = row < p.M;
-            const int64_t col0 = (int64_t)nb * kGemmBN;
+            const int64_t col0 = (int64_t)nb * BN;
 #pragma unroll 1
-            for (int c0 = 0; c0 < kGemmBN; c0 += 32) {
+            for (int c0 = 0; c0 < BN; c0 += 32) {
                 uint32_t r[32];
-                tmem_ld32_sync(tmem + lane_base + (uint32_t)(buf * kGemmBN + c0), r);
+                tmem_ld32_sync(tmem + lane_base + (uint32_t)(buf * kGemmD + c0), r);
                 const int64_t col = col0 + c0;
                 if (!row_ok || col >= p.N) continue;
                 store_row32(p, r, row, col);
@@ -532,15 +550,45 @@ namespace nomas {
 
 static bool pitch_ok(int64_t ld, int64_t k) { return ld >= k && ld % 8 == 0; }
 
+typedef void (*GemmKernel)(const CUtensorMap, const CUtensorMap, const GemmParams);
+struct GemmWidth {
+    int columns, smem;
+    GemmKernel kernel;
+};
+static const GemmWidth kWidths[] = {{256, GemmCfg<256>::SMEM, gemm_bf16_kernel<256>}, {128, GemmCfg<128>::SMEM, gemm_bf16_kernel<128>}};
+static const GemmWidth kPairWidths[] = {{256, Gemm2Cfg<256>::SMEM, gemm2_bf16_kernel<256>},
+                                        {224, Gemm2Cfg<224>::SMEM, gemm2_bf16_kernel<224>},
+                                        {192, Gemm2Cfg<192>::SMEM, gemm2_bf16_kernel<192>}};
+
 static int gemm_attr() {
     static std::once_flag once;
     static cudaError_t e = cudaSuccess;
     std::call_once(once, [] {
-        e = cudaFuncSetAttribute(gemm_bf16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmCfg::SMEM);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(gemm2_bf16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Gemm2Cfg::SMEM);
+        auto allow = [](const GemmWidth &w) {
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(reinterpret_cast<const void *>(w.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, w.smem);
+        };
+        for (const GemmWidth &w : kWidths) allow(w);
+        for (const GemmWidth &w : kPairWidths) allow(w);
     });
     return e == cudaSuccess ? NOMAS_OK : cuda_fail("cudaFuncSetAttribute(gemm smem)", (int)e, cudaGetErrorString(e));
+}
+
+// The width of tile that takes least time: rounds of `at_once` tiles, each as long as its columns and a part that does
+// not depend on them.  The sums do not depend on the width.  Measured in us (256 / 224 / 192 columns, SM pairs):
+// 26400 x 2048 -> 6144 445 / 484 / 522, 1280 x 2048 -> 8192 37 / 35 / 34 (3 rounds each), 1760 x 2048 -> 6144
+// 42 / 37 / 40 (3, 3, 4), 880 x 8192 -> 2048 43 / 39 / 35 (one); (256 / 128, one SM a tile) 128 x 2048 -> 12288 20 / 14,
+// x 8192 -> 8192 53 / 35, x 2048 -> 28001 25 / 26 (1, 2).
+static const GemmWidth &pick_width(bool pair, int64_t m_blocks, int64_t n_out, int64_t at_once) {
+    const GemmWidth *best = nullptr, *const all = pair ? kPairWidths : kWidths;
+    const int count = pair ? 3 : 2, apart = pair ? 210 : 100;
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < count; ++i) {
+        const int64_t tiles = m_blocks * ((n_out + all[i].columns - 1) / all[i].columns);
+        const int64_t cost = (tiles + at_once - 1) / at_once * (all[i].columns + apart);
+        if (cost < least) least = cost, best = &all[i];
+    }
+    return *best;
 }
 
 static int check_linear(const void *x, int64_t m, int64_t k_in, int64_t ldx, const void *w, int64_t n_out,
@@ -560,13 +608,15 @@ static int enqueue_linear(const void *x, int64_t m, int64_t k_in, int64_t ldx, c
     CUtensorMap ta, tb;
     const cuuint64_t da[3] = {(cuuint64_t)k_in, (cuuint64_t)m, 1};
     const cuuint64_t sa[2] = {(cuuint64_t)ldx * 2, (cuuint64_t)ldx * 2 * (cuuint64_t)m};
-    // SM pairs (256 x 256 tiles, 128 rows of A and of B per CTA) unless there is one pair's worth of rows
-    // or less; then one SM per 128 x 256 tile
+    // SM pairs (tiles of 256 rows, 128 a CTA, which also stages half of B's) unless there is one pair's worth of rows or
+    // less; then one SM per tile of 128 rows
     const bool pair = m > 128 && sm_count() >= 2;
+    const int64_t at_once = pair ? sm_count() / 2 : sm_count(), m_blocks = (m + (pair ? 255 : kGemmBM - 1)) / (pair ? 256 : kGemmBM);
+    const GemmWidth &width = pick_width(pair, m_blocks, n_out, at_once);
     const cuuint32_t ba[3] = {kGemmBK, kGemmBM, 1};
     const cuuint64_t db[3] = {(cuuint64_t)k_in, (cuuint64_t)n_out, 1};
     const cuuint64_t sb[2] = {(cuuint64_t)ldw * 2, (cuuint64_t)ldw * 2 * (cuuint64_t)n_out};
-    const cuuint32_t bb[3] = {kGemmBK, pair ? 128u : (cuuint32_t)kGemmBN, 1};
+    const cuuint32_t bb[3] = {kGemmBK, (cuuint32_t)(pair ? width.columns / 2 : width.columns), 1};
     if (!make_tensor_map_3d(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, da, sa, ba, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_tensor_map_3d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w, db, sb, bb, CU_TENSOR_MAP_SWIZZLE_128B))
         return NOMAS_ECUDA;
@@ -574,24 +624,17 @@ static int enqueue_linear(const void *x, int64_t m, int64_t k_in, int64_t ldx, c
     p.M = m;
     p.N = n_out;
     p.k_iters = (int32_t)((k_in + kGemmBK - 1) / kGemmBK);
-    p.n_nblk = (int32_t)((n_out + kGemmBN - 1) / kGemmBN);
-    p.n_tiles = (int64_t)p.n_nblk * ((m + (pair ? 256 : kGemmBM) - 1) / (pair ? 256 : kGemmBM));
+    p.n_nblk = (int32_t)((n_out + width.columns - 1) / width.columns);
+    p.n_tiles = p.n_nblk * m_blocks;
     p.y = y;
     p.ldy = ldy;
     p.y_bf16 = y_dtype == NOMAS_DTYPE_BF16;
     p.y_vec = ldy % (p.y_bf16 ? 8 : 4) == 0;
     p.err = status;
     p.timeout_ns = wait_limit_ns();
-    if (pair) {
-        int64_t pairs = sm_count() / 2;
-        if (pairs > p.n_tiles) pairs = p.n_tiles;
-        gemm2_bf16_kernel<<<(unsigned)(2 * pairs), kGemmThreads, Gemm2Cfg::SMEM, st>>>(ta, tb, p);
-        return check_launch("gemm2_bf16_kernel launch");
-    }
-    int64_t grid = sm_count();
-    if (grid > p.n_tiles) grid = p.n_tiles;
-    gemm_bf16_kernel<<<(unsigned)grid, kGemmThreads, GemmCfg::SMEM, st>>>(ta, tb, p);
-    return check_launch("gemm_bf16_kernel launch");
+    const int64_t grid = (at_once < p.n_tiles ? at_once : p.n_tiles) * (pair ? 2 : 1);
+    width.kernel<<<(unsigned)grid, kGemmThreads, width.smem, st>>>(ta, tb, p);
+    return check_launch(pair ? "gemm2_bf16_kernel launch" : "gemm_bf16_kernel launch");
 }
 
 static int enqueue_dequant(const int8_t *codes, const float *scales, int64_t n_out, int64_t k_in, void *w,

@@ -370,30 +370,33 @@ __global__ void __launch_bounds__(kTileThreads + 32, 2) w4_tile_kernel(const __g
     // most waits find their phase complete: a test first (try_wait alone cost 240 cycles)
     auto wait = [&](uint64_t *bar, int phase, int site) { return mbar_test_wait(bar, phase & 1) || mbar_wait(bar, phase & 1, wd, site); };
     if (warp == kTileThreads / 32) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, NX);
+        constexpr uint32_t idesc = idesc_bf16_f32(kTileRows, NX);
+        const uint32_t d_tmem = __shfl_sync(0xffffffffu, tmem, 0);
+        if (elect_one())
             for (int s = first; s < min(first + STAGES, last); ++s) fetch(s);
-            int u = 0;
-            for (; u < halves; ++u) {
-                const int j = u & 1;
-                if (!wait(&ready[j], u >> 1, 3)) break;
-                tc_fence_after();
+        int u = 0;
+        for (; u < halves; ++u) {
+            const int j = u & 1;
+            if (!__all_sync(0xffffffffu, wait(&ready[j], u >> 1, 3))) break;
+            tc_fence_after();
+            if (elect_one()) {
                 const uint64_t xd = sdesc_sw128(smem_u32(sx) + j * XHALF, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    umma_ts(tmem + kTileD + ((u >> 2) & 1) * NX, tmem + j * 64 + 8 * k, xd + ((k / 4) * XBLOCK + (k % 4) * 32) / 16, idesc,
-                            k > 0 || (u & 3) ? 1u : 0u);
+                    umma_ts(d_tmem + kTileD + ((u >> 2) & 1) * NX, d_tmem + j * 64 + 8 * k, xd + ((k / 4) * XBLOCK + (k % 4) * 32) / 16,
+                            idesc, k > 0 || (u & 3) ? 1u : 0u);
                 umma_commit(&done[j]);
                 // both halves of the slab are widened: its stage is free
                 const int to = first + (u >> 1) + STAGES;
                 if (j == 1 && to < last) fetch(to);
             }
-            if (u < halves) {
-                // a wait ran out: products and copies in flight must end before TMEM and shared memory go
-                for (int v = max(0, u - 2); v < u; ++v) mbar_drain(&done[v & 1], (v >> 1) & 1, 100000000ull);
-                for (int s = u >> 1; s < min((u >> 1) + STAGES, last - first); ++s)
-                    mbar_drain(&full[s % STAGES], (s / STAGES) & 1, 100000000ull);
-            }
+            __syncwarp();
+        }
+        if (u < halves && lane == 0) {
+            // a wait ran out: products and copies in flight must end before TMEM and shared memory go
+            for (int v = max(0, u - 2); v < u; ++v) mbar_drain(&done[v & 1], (v >> 1) & 1, 100000000ull);
+            for (int s = u >> 1; s < min((u >> 1) + STAGES, last - first); ++s)
+                mbar_drain(&full[s % STAGES], (s / STAGES) & 1, 100000000ull);
         }
         __syncwarp();
     } else {
@@ -623,9 +626,9 @@ static int enqueue_w4_sums(const void *x, int64_t m, int64_t k_in, int64_t ldx, 
     return NOMAS_OK;
 }
 
-// Rows of x that need no GEMM: up to 128 of them its 128 x 256 tiles leave most SMs idle below 4096 rows of W, and walk
-// long rows one after the other (us, GEMM against this file's kernels: 128 x 4096 -> 4096 39 / 21, x 8192 -> 8192 84 / 65,
-// x 2048 -> 12288 27 / 36).
+// Rows of x that need no GEMM: up to 128 of them the widened weights' way through memory costs more than it saves where
+// rows are long, or W small (us, GEMM with its dequantise pass against this file's kernels: 128 x 2048 -> 2048 13 / 12,
+// x 4096 -> 4096 23 / 25, x 8192 -> 2048 36 / 23, x 8192 -> 8192 65 / 57, x 2048 -> 12288 21 / 36).
 static bool w4_few(int64_t m, int64_t n_out, int64_t k_in) {
     if (m <= NOMAS_W4_FEW_ROWS || (m <= 128 && (n_out <= 4096 || k_in >= 4096))) return true;
     // products that take less than the GEMM's launches (some 20 us)
@@ -687,7 +690,7 @@ static int pick_w4_rows(const W4Params &p, cudaStream_t st) {
 
 // Whether few rows of x go to w4_tile_kernel rather than w4_rows_kernel, which takes 32 of them at a time and has less
 // to set up (us, rows against tiles: 64 x 8192 -> 8192 64 / 32, x 2048 -> 12288 28 / 20, x 4096 -> 4096 19 / 15,
-// x 2048 -> 2048 8 / 11; 30 x 8192 -> 8192 32 / 26, x 2048 -> 12288 14 / 17; 128 x 2048 -> 2048 15 / 12).
+// x 2048 -> 2048 8 / 11; 30 x 8192 -> 8192 32 / 25, x 2048 -> 12288 14 / 17; 128 x 2048 -> 2048 15 / 12).
 static bool w4_tiles(int64_t m, int64_t n_out, int64_t k_in) {
     const int64_t weights = n_out * k_in;
     return m > 64 ? weights >= 1 << 22 : m > 32 ? weights >= 1 << 23 : m > 16 && weights >= 1 << 26;
