@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_bf16_kernel(const __grid
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_wait();                        // the previous grid of the stream has completed (programmatic launch)
     const uint32_t tmem = misc[0];
     Watchdog wd{p.err, abort_flag, p.timeout_ns, 9};
 
@@ -426,6 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     tc_fence_before();
     cluster_sync_all();                    // both CTAs' barriers are initialised before any remote use
     tc_fence_after();
+    griddep_wait();                        // the previous grid of the stream has completed (programmatic launch)
     const uint32_t tmem = misc[0];
     Watchdog wd{p.err, abort_flag, p.timeout_ns, 9};
 
@@ -633,8 +635,8 @@ static int enqueue_linear(const void *x, int64_t m, int64_t k_in, int64_t ldx, c
     p.err = status;
     p.timeout_ns = wait_limit_ns();
     const int64_t grid = (at_once < p.n_tiles ? at_once : p.n_tiles) * (pair ? 2 : 1);
-    width.kernel<<<(unsigned)grid, kGemmThreads, width.smem, st>>>(ta, tb, p);
-    return check_launch(pair ? "gemm2_bf16_kernel launch" : "gemm_bf16_kernel launch");
+    const cudaError_t e = launch_pdl(width.kernel, dim3((unsigned)grid), dim3(kGemmThreads), width.smem, st, ta, tb, p);
+    return e == cudaSuccess ? NOMAS_OK : cuda_fail(pair ? "gemm2_bf16_kernel launch" : "gemm_bf16_kernel launch", (int)e, cudaGetErrorString(e));
 }
 
 static int enqueue_dequant(const int8_t *codes, const float *scales, int64_t n_out, int64_t k_in, void *w,
