@@ -922,7 +922,7 @@ static int pick_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     if constexpr (CH == 1) {
         if (p.cols <= 2048) return launch_bwd<TX, TY, 1, 8, 1, 256, true>(p, ctas, st);
         p.team_log2 = 9;
-        if (p.cols <= 4096) return launch_bwd<TX, TY, 1, 8, 1, 512, true>(p, ctas, st);
+        if (p.cols <= 4096) return launch_bwd<TX, TY, 1, 8, 2, 512, true>(p, ctas, st);
     } else {
         if (p.cols <= 2048) return launch_bwd<TX, TY, CH, 8 / CH, 4, 256, true>(p, ctas, st);
         if (p.cols <= 4096) return launch_bwd<TX, TY, CH, 16 / CH, 2, 256, true>(p, ctas, st);
