@@ -15,8 +15,8 @@
 //                        the next); four epilogue warps per CTA read them with tcgen05.ld.
 //   gemm_bf16_kernel     the same on one SM per 128 x 256 (or 128) tile (SS tcgen05.mma M128 K16), for at
 //                        most 128 rows.
+#include <atomic>
 #include <cstdio>
-#include <mutex>
 
 #include "common.cuh"
 #include "quant.cuh"
@@ -562,18 +562,21 @@ static const GemmWidth kPairWidths[] = {{256, Gemm2Cfg<256>::SMEM, gemm2_bf16_ke
                                         {224, Gemm2Cfg<224>::SMEM, gemm2_bf16_kernel<224>},
                                         {192, Gemm2Cfg<192>::SMEM, gemm2_bf16_kernel<192>}};
 
+// Allows the kernels their shared memory, once a device.
 static int gemm_attr() {
-    static std::once_flag once;
-    static cudaError_t e = cudaSuccess;
-    std::call_once(once, [] {
-        auto allow = [](const GemmWidth &w) {
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(reinterpret_cast<const void *>(w.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, w.smem);
-        };
-        for (const GemmWidth &w : kWidths) allow(w);
-        for (const GemmWidth &w : kPairWidths) allow(w);
-    });
-    return e == cudaSuccess ? NOMAS_OK : cuda_fail("cudaFuncSetAttribute(gemm smem)", (int)e, cudaGetErrorString(e));
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64 && (allowed.load() >> dev & 1)) return NOMAS_OK;
+    auto allow = [&e](const GemmWidth &w) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(reinterpret_cast<const void *>(w.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, w.smem);
+    };
+    for (const GemmWidth &w : kWidths) allow(w);
+    for (const GemmWidth &w : kPairWidths) allow(w);
+    if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(gemm smem)", (int)e, cudaGetErrorString(e));
+    if (dev < 64) allowed.fetch_or((uint64_t)1 << dev);
+    return NOMAS_OK;
 }
 
 // The width of tile that takes least time: rounds of `at_once` tiles, each as long as its columns and a part that does
