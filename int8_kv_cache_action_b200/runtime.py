@@ -557,13 +557,14 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
         if s.dtype != torch.float32 or s.shape != (rows,) or not s.is_contiguous():
             raise ValueError("mean, rstd: contiguous fp32 [rows]")
     _same_device(x, dy, mean, rstd, weight)
-    device = x.device
     dx = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dx else None
     dw = db = ws = None
     if want_params:
         dw = x.new_empty((groups, cols), dtype=torch.float32)
         db = torch.empty_like(dw)
-        ws = torch.empty(N.lib.nomas_layernorm_workspace_bytes(rows, cols, rows_per_group), dtype=torch.uint8, device=device)
+        need = N.lib.nomas_layernorm_workspace_bytes(rows, cols, rows_per_group)
+        if need > 16:                                         # 16: nothing to add up across shares
+            ws = x.new_empty(need, dtype=torch.uint8)
     if rows and (want_dx or want_params):
         N._check(N.lib.nomas_layernorm_bwd(dy.data_ptr(), _pitch(dy), _DTYPES[dy.dtype], x.data_ptr(), _pitch(x),
                                            _DTYPES[x.dtype], rows, cols, _ptr(weight), pitch, p_dtype, rows_per_group,
