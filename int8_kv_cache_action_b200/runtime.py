@@ -493,7 +493,7 @@ def _norm_params(x, weight, bias, rows_per_group):
     if weight is None and bias is None:
         return cols, N.NOMAS_DTYPE_F32, -(-rows // rows_per_group) if rows_per_group else 1
     groups = -(-rows // rows_per_group) if rows_per_group else 1
-    pitch, dtype = 0, None
+    pitch = dtype = None
     for p in (weight, bias):
         if p is None:
             continue
@@ -503,10 +503,12 @@ def _norm_params(x, weight, bias, rows_per_group):
         if shape != (groups, cols) or p.dtype not in _DTYPES or strides[1] != 1:
             raise ValueError("weight, bias: bf16 or fp32 [groups, C] ([C] for one group) with contiguous rows")
         at = strides[0] if groups > 1 else cols
+        if at < cols:
+            raise ValueError("weight, bias: a row of its own for every group, not an expanded or overlapping one")
         if dtype is not None and (at != pitch or p.dtype != dtype):
             raise ValueError("weight and bias must share their type and strides")
         pitch, dtype = at, p.dtype
-    return pitch or cols, _DTYPES[dtype or torch.float32], groups
+    return pitch, _DTYPES[dtype], groups
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,

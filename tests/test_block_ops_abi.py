@@ -79,3 +79,20 @@ def test_w4_refusals(N):
     assert N.nomas_w4_quantize(0, 16, 64, 64, 64, A, A) == N.NOMAS_EINVAL
     assert N.nomas_w4_quantize(A, 16, 64, 63, 64, A, A) == N.NOMAS_EINVAL
     assert N.nomas_w4_dequant(A, A, 64, 16, 64, A + 8) == N.NOMAS_EINVAL
+
+
+def test_layernorm_parameter_rows_that_overlap_are_refused(N):
+    # a group's row is read at its pitch from the first, so an expanded row (stride 0) must never reach a launch
+    import torch
+    from int8_kv_cache_action_b200.runtime import _norm_params
+    x, row = torch.zeros((8, 64)), torch.zeros(64)
+    expanded, overlapping = row.expand(4, 64), torch.zeros(4 * 63 + 1).as_strided((4, 64), (63, 1))
+    for p in (expanded, overlapping):
+        for weight, bias in ((p, None), (None, p), (p, p)):
+            with pytest.raises(ValueError):
+                _norm_params(x, weight, bias, 2)
+    assert _norm_params(x, row.expand(1, 64), row, 0) == (64, N.NOMAS_DTYPE_F32, 1)      # one group: its only row
+    views = torch.zeros((4, 128), dtype=torch.bfloat16)
+    assert _norm_params(x, views[:, 64:], views[:, :64], 2) == (128, N.NOMAS_DTYPE_BF16, 4)
+    assert _norm_params(x, None, None, 2) == (64, N.NOMAS_DTYPE_F32, 4)
+    assert _norm_params(x[:0], expanded[:0], None, 2)[2] == 0

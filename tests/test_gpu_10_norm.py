@@ -222,3 +222,15 @@ def test_refusals():
         layer_norm(torch.zeros((2, N.NOMAS_NORM_MAX_COLS + 1), device="cuda"))
     with pytest.raises(N.NomasError):
         layer_norm(x, eps=-1.0)
+
+
+def test_expanded_parameters_are_refused():
+    x = _randn((8, 64), BF16, 28)
+    p = _randn((64,), BF16, 29).expand(4, 64)
+    _, mean, rstd = layer_norm(x, want_stats=True)
+    for weight, bias in ((p, None), (None, p), (p, p)):
+        with pytest.raises(ValueError):
+            layer_norm(x, weight, bias, rows_per_group=2)
+    with pytest.raises(ValueError):
+        layer_norm_backward(x, x, mean, rstd, p, rows_per_group=2)
+    _check_forward(x, p.contiguous(), p.contiguous(), 2, True, BF16)
