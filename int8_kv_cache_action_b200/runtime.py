@@ -469,13 +469,14 @@ class AxisRope:
                 if y.shape != shape or y.dtype != dtype or sy[2] != 1 or y.get_device() != index:
                     raise ValueError("out: tensors of the inputs' shape, type and device with contiguous head_dim")
             ys.append(y)
-            # a single token's or head's stride says nothing
-            args += (x.data_ptr(), y.data_ptr(), sx[0] if t > 1 else 0, sx[1] if h > 1 else 0, sy[0] if t > 1 else 0,
-                     sy[1] if h > 1 else 0, h, 0)
-        if t and min(args[6::8]):
+            if h:                          # a tensor without heads has nothing to turn
+                # a single token's or head's stride says nothing
+                args += (x.data_ptr(), y.data_ptr(), sx[0] if t > 1 else 0, sx[1] if h > 1 else 0, sy[0] if t > 1 else 0,
+                         sy[1] if h > 1 else 0, h, 0)
+        if t and args:
             N._check(N.lib.nomas_rope(self._spec, None if grid is None else ctypes.byref(grid),
                                       None if positions is None else positions.data_ptr(), t, N.pack_rope_tensors(args),
-                                      len(xs), _DTYPES[dtype], inverse, st), "nomas_rope")
+                                      len(args) // 8, _DTYPES[dtype], inverse, st), "nomas_rope")
         return ys[0] if single else tuple(ys)
 
 

@@ -162,3 +162,17 @@ def test_refusals():
     host = torch.zeros((4, 2, 128), dtype=BF16).pin_memory()   # host memory handed to the C call
     args = N.make_rope_tensors([(host.data_ptr(), host.data_ptr(), 256, 128, 256, 128, 2)])
     assert N.nomas_rope(rope.spec, g, 0, 4, args, 1, N.NOMAS_DTYPE_BF16, 0) == N.NOMAS_EINVAL
+
+
+@pytest.mark.parametrize("pairing", ["interleaved", "halves"])
+def test_a_tensor_without_heads_leaves_the_others_turned(pairing):
+    rope, g = AxisRope(128, (16, 56, 56), pairing=pairing), rope_grid(2, 3)
+    q, none = _randn((9, 16, 128), BF16, 13).cuda(), torch.empty((9, 0, 128), dtype=BF16, device="cuda")
+    ref = rope(q, grid=g)
+    for xs, at in (((q, none), 0), ((none, q), 1), ((none, q, none), 1)):
+        out = tuple(torch.full_like(x, 3.0) for x in xs)
+        got = rope(xs, grid=g, out=out)
+        assert torch.equal(got[at], ref) and all(y is o for y, o in zip(got, out))
+        assert torch.equal(rope(xs, grid=g)[at], ref)
+        assert all(y.shape == x.shape for y, x in zip(got, xs))
+    assert rope(none, grid=g).shape == none.shape and rope((none, none), grid=g)[1].shape == none.shape
