@@ -642,20 +642,37 @@ __global__ void __launch_bounds__(T, T == 256 ? 2 : 1) layernorm_bwd_kernel(cons
             if constexpr (!RING) fetch_registers();
             last = stage;
             stage = stage + 1 == S ? 0 : stage + 1;
-            // columns past the row and rows past the group have dy = 0: what their xhat is adds nothing
+            // rows past the group have dy = mean = rstd = 0 and add nothing.  Columns past the row have dy = 0, but x = 0 too,
+            // whose xhat, -mean rstd, can overflow where every xhat of the row is small: it stays out of the second sum (odd
+            // widths, whose pairs can end inside the row, take the mean for x)
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const Pair minus = pair_of(-mean[r], -mean[r]), scale = pair_of(rstd[r], rstd[r]);
                 Pair s1 = 0, s2 = 0;
 #pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    const Pair xv = mul2(add2(xh[r][k], minus), scale), d = gy[r][k], gv = mul2(d, f[k]);
-                    aw[k] = fma2(d, xv, aw[k]);
-                    ab[k] = add2(ab[k], d);
-                    s1 = add2(s1, gv);
-                    s2 = fma2(gv, xv, s2);
-                    xh[r][k] = xv;
-                    gy[r][k] = gv;
+                for (int j = 0; j < NV; ++j) {
+                    const bool in = (uint32_t)(lane + j * team) * CH < p.cols;
+                    if constexpr (CH == 1) {    // a pair is two chunks
+                        if (!in) {
+                            float lo, hi;
+                            pair_split(xh[r][j / 2], lo, hi);
+                            (j & 1 ? hi : lo) = mean[r];
+                            xh[r][j / 2] = pair_of(lo, hi);
+                        }
+                        if ((j & 1) == 0) continue;
+                    }
+                    const Pair before = s2;
+#pragma unroll
+                    for (int k = CH == 1 ? j / 2 : j * CH / 2; k < (j + 1) * CH / 2; ++k) {
+                        const Pair xv = mul2(add2(xh[r][k], minus), scale), d = gy[r][k], gv = mul2(d, f[k]);
+                        aw[k] = fma2(d, xv, aw[k]);
+                        ab[k] = add2(ab[k], d);
+                        s1 = add2(s1, gv);
+                        s2 = fma2(gv, xv, s2);
+                        xh[r][k] = xv;
+                        gy[r][k] = gv;
+                    }
+                    if (CH > 1 && !in) s2 = before;
                 }
                 s[2 * r] = pair_sum(s1);
                 s[2 * r + 1] = pair_sum(s2);

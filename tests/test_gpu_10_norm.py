@@ -234,3 +234,15 @@ def test_expanded_parameters_are_refused():
     with pytest.raises(ValueError):
         layer_norm_backward(x, x, mean, rstd, p, rows_per_group=2)
     _check_forward(x, p.contiguous(), p.contiguous(), 2, True, BF16)
+
+
+@pytest.mark.parametrize("cols", [71, 72, 1096, 1100, 3000, 3001, 5000, 5001, 9000, 9001])
+@pytest.mark.parametrize("xt,yt", [(BF16, BF16), (F32, F32), (F32, BF16)])
+def test_backward_of_a_row_whose_mean_times_rstd_overflows(cols, xt, yt):
+    # every xhat of the constant row is 0, but (0 - mean) rstd, what padding past the row would have, is -infinity
+    x, dy, w = _randn((6, cols), xt, 30), _randn((6, cols), yt, 31), _randn((cols,), F32, 32)
+    _, mean, rstd = layer_norm(x, want_stats=True)
+    x[2] = 4.0e35
+    mean[2], rstd[2] = x[2, 0].float(), 1000.0
+    _check_backward(dy, x, mean, rstd, w, 0, False)
+    _check_backward(dy, x, mean, rstd, None, 2, True)
