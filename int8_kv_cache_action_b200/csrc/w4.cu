@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kTileThreads + 32, 2) w4_tile_kernel(const __g
                 v[i] = __ldg(reinterpret_cast<const uint4 *>(p.x + (int64_t)(m0 + xr) * p.ldx + col));
         }
     };
-    // scales of the slabs from `slab` on; zeros past the columns, whose codes TMA fills with zeros (code -8)
+    // scales of the slabs from `slab` on; zeros past the last group
     auto load_scales = [&](int slab) {
         constexpr int U = 8;                   // loads in flight
         const int left = last - slab, g0 = slab * kSlab >> p.group_log2;
@@ -412,6 +412,9 @@ __global__ void __launch_bounds__(kTileThreads + 32, 2) w4_tile_kernel(const __g
                 for (int i = 0; i < 16; ++i) acc[c + i] += d[i];
             }
         };
+        // past the columns TMA fills with zeros, which are the code -8: its product with the scale of a group that K ends in
+        // can overflow, and meets zeros of x, so the scale is 0 there (32 columns are in or past together)
+        const int columns = p.k - first * kSlab - part_of * 64;
         int u = 0, collected = 0;
         for (; u < halves; ++u) {
             const int it = u >> 1, j = u & 1, s = it % STAGES;
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(kTileThreads + 32, 2) w4_tile_kernel(const __g
             const int col0 = (it % kScaleSlabs) * kSlab + j * 128 + part_of * 64;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const __nv_bfloat16 f = sr[(col0 + q * 32) >> p.group_log2];
+                const __nv_bfloat16 f = u * 128 + q * 32 < columns ? sr[(col0 + q * 32) >> p.group_log2] : __float2bfloat16_rn(0.0f);
                 const uint4 w = *reinterpret_cast<const uint4 *>(sw + s * kTileStage + sw128_offset(row_in, j * 4 + part_of * 2 + q));
                 const __nv_bfloat162 sc = __halves2bfloat162(f, f);
                 uint32_t r[16];

@@ -212,3 +212,18 @@ def test_refusals():
             Int4Linear(*bad)
     with pytest.raises(ValueError):
         Int4Linear.from_weights(torch.zeros((4, 48), dtype=BF16, device="cuda"))
+
+
+@pytest.mark.parametrize("m,n,k,group", [(64, 4096, 4128, 64), (64, 4096, 4160, 128), (100, 1030, 4128, 128), (20, 16500, 4128, 64),
+                                         (8, 200, 96, 64), (30, 300, 1056, 128), (200, 2100, 1056, 128)])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+def test_scales_near_the_largest_of_a_last_group_that_columns_end_in(m, n, k, group, out_dtype):
+    # codes of at most 4 in size: every weight is at most 2e38 and finite; past column K, 8 times the scale is not
+    g = torch.Generator().manual_seed(22)
+    c = torch.randint(4, 13, (n, k), generator=g, dtype=torch.int32)
+    codes = (c[:, 0::2] | c[:, 1::2] << 4).to(torch.uint8)
+    lin = Int4Linear(codes.cuda(), torch.full((n, -(-k // group)), 5.0e37, dtype=BF16, device="cuda"), group)
+    x = (torch.randn(m, k, generator=g) * 1e-20).to(BF16).cuda()
+    y = lin(x, out_dtype=out_dtype)
+    assert lin.status() == N.NOMAS_OK
+    _check(y, x, lin)
