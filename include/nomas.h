@@ -380,7 +380,10 @@ int nomas_status_read(int32_t *status, nomas_stream stream);
  *       y1 = x1 cos - x2 sin,   y2 = x1 sin + x2 cos
  *   inverse != 0 turns by the negative angle: the inverse, and the gradient with respect to x of a
  *   gradient with respect to y (a rotation's adjoint is its inverse).
- * Angles are reduced in fp64, sines and products are fp32, the result is rounded once to the type.
+ * Sines and products are fp32, the result is rounded once to the type.  Angles are reduced before: the turns of a
+ * grid position (its pair's turns per unit held to 2^-55, products of 64-bit mantissas, the index times the step in
+ * whole numbers) are off by at most 2^-55 of their number and 2^-32, those of a given position, fp64 products, by
+ * at most 2^-51 of their number.
  * ------------------------------------------------------------------------------------------ */
 #define NOMAS_ROPE_INTERLEAVED 0
 #define NOMAS_ROPE_HALVES 1
@@ -419,8 +422,7 @@ typedef struct {
  *   positions  fp32 [tokens][3] (device): time, height, width of each token; exactly one
  *              of grid and positions is given.  A non-finite position gives NaN in its axis' channels.
  *   dtype      NOMAS_DTYPE_BF16 or NOMAS_DTYPE_F32, of every x and y
- * Positions, origins and steps times a pair's turns must stay finite in fp64; a grid's far indices keep full
- * precision, a given position that of its fp32.
+ * Positions, origins and steps times a pair's turns must stay finite in fp64.
  * tokens = 0 does nothing.  Runs on the device that holds the first tensor.  Errors: NOMAS_EINVAL for a
  * bad pointer, stride, spec or grid; NOMAS_EUNSUPPORTED for 2^31 tokens or more. */
 int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *grid, const float *positions, int64_t tokens,

@@ -357,10 +357,10 @@ static int launch_rope(dim3 grid, unsigned threads, const RopeParams &p, cudaStr
     return check_launch("rope_kernel launch");
 }
 
-// The fraction of a number of turns, in 2^-64.
-static int64_t rope_fraction(double turns) {
-    const double part = turns - std::nearbyint(turns);                 // exact, -1/2 .. 1/2
-    return (int64_t)((uint64_t)std::llrint(part * 0x1p62) << 2);
+// The fraction of a number of turns, in 2^-64.  In long double: an index of the grid multiplies the rounding.
+static int64_t rope_fraction(long double turns) {
+    const long double part = turns - std::nearbyint(turns);            // exact, -1/2 .. 1/2
+    return (int64_t)((uint64_t)std::llrint(part * 0x1p63L) << 1);
 }
 
 static bool rope_spec_ok(const nomas_rope_spec *s) {
@@ -439,7 +439,8 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
         if (items >= (int64_t)1 << 24) return NOMAS_EUNSUPPORTED;      // 512 a CTA along a grid's y
     }
     if (tokens == 0) return NOMAS_OK;
-    // theta^(-2 i / d) as powers of one root: 128 products in the 64-bit mantissa of long double stay exact to fp64
+    // theta^(-2 i / d) as powers of one root: 127 products in the 64-bit mantissa of long double, each off by 2^-64 and by
+    // the root's 2^-63, stay exact to 2^-55
     int pair = 0;
     for (int a = 0; a < 3; ++a) {
         if (spec->axis_dim[a] == 0) continue;
@@ -450,7 +451,7 @@ extern "C" int nomas_rope(const nomas_rope_spec *spec, const nomas_rope_grid *gr
             if (!std::isfinite(turns) || (grid && (!std::isfinite(turns * grid->origin[a]) || !std::isfinite(turns * grid->step[a]))))
                 return NOMAS_EINVAL;
             if (grid)
-                p.pair[pair] = RopePair{rope_fraction(turns * grid->origin[a]), rope_fraction(turns * grid->step[a])};
+                p.pair[pair] = RopePair{rope_fraction(at * grid->origin[a]), rope_fraction(at * grid->step[a])};
             else
                 std::memcpy(&p.pair[pair].origin, &turns, sizeof(turns));
         }

@@ -2,6 +2,8 @@
 one rounding to the type (half a step, eps / 2 relative): the angle, held in fp32 turns after an fp64 reduction
 (|angle| <= pi, relative 2^-24), sine and cosine (2 ulp of at most 2^-24 each), two products and a sum: under
 2^-20 (|x1| + |x2|) in all."""
+from decimal import Decimal, getcontext
+
 import numpy as np
 import pytest
 import torch
@@ -176,3 +178,27 @@ def test_a_tensor_without_heads_leaves_the_others_turned(pairing):
         assert torch.equal(rope(xs, grid=g)[at], ref)
         assert all(y.shape == x.shape for y, x in zip(got, xs))
     assert rope(none, grid=g).shape == none.shape and rope((none, none), grid=g)[1].shape == none.shape
+
+
+@pytest.mark.parametrize("dtype,pairing", [(F32, "interleaved"), (F32, "halves"), (BF16, "interleaved")])
+def test_far_indices_of_a_grid(dtype, pairing):
+    # positions up to 1e12, 1.6e11 turns, against 60 digits.  Beside the sines' 2^-20, pair i's turns are off by (1.5 i + 2)
+    # 2^-63 of their number (i products and the root's powers, the step's product) and 3000 2^-64 of a turn
+    getcontext().prec = 60
+    two_pi = Decimal("6.28318530717958647692528676655900576839433879875021164194988918")
+    step, origin, t = 1.0e9 / 3.0, -1.0e11 / 7.0, 3001
+    x = torch.zeros((t, 1, 16), dtype=dtype, device="cuda")
+    first = slice(0, 8) if pairing == "halves" else slice(0, 16, 2)
+    second = slice(8, 16) if pairing == "halves" else slice(1, 16, 2)
+    x[..., first] = 1.0                                       # y is the cosines and sines themselves
+    y = AxisRope(16, (16, 0, 0), pairing=pairing)(x, grid=rope_grid(1, 1, (origin, 0.0, 0.0), (step, 0.0, 0.0)))
+    y = y[:, 0].double().cpu().numpy()
+    round_off = torch.finfo(dtype).eps / 2
+    for n in [0, 1, 2, 3000, *range(7, t, 101)]:
+        for i in range(8):
+            turns = (Decimal(origin) + n * Decimal(step)) * (-(Decimal(2 * i) / 16) * Decimal(10000).ln()).exp() / two_pi
+            size = abs(origin) + n * step
+            a = 2 * np.pi * float(turns - turns.to_integral_value())
+            slack = 2.0 ** -20 + 2 * np.pi * ((1.5 * i + 2) * 2.0 ** -63 * size * 10000.0 ** (-i / 8) / 6.28 + 3002 * 2.0 ** -64)
+            for got, ref in ((y[n, first][i], np.cos(a)), (y[n, second][i], np.sin(a))):
+                assert abs(got - ref) <= slack + round_off * (abs(ref) + slack), (n, i)
