@@ -80,3 +80,49 @@ def test_calls_behind_one_another_see_each_other(m, n, k):
         _call(mid, back, out)
     side.synchronize()
     assert torch.equal(out, expect[0]) and not any(s.any() for s in states)
+
+
+@pytest.mark.parametrize("m,n,k", [(96, 12288, 1024), (640, 8192, 1024), (1300, 6144, 2048)])
+def test_products_directly_behind_one_another(m, n, k):
+    # nothing stands between the products of a chain: a product is launched as the one that writes its input retires.  All
+    # that they need is allocated, and their results are overwritten, before the chain starts
+    x, w = _inputs(m, n, k, 4)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    back = (torch.randn(k, n, generator=g, device="cuda") / (k * n) ** 0.5).to(BF16)
+    links, status = 4, torch.zeros(4, dtype=torch.int32, device="cuda")
+    bufs = [torch.empty((m, n if i % 2 == 0 else k), dtype=BF16, device="cuda") for i in range(2 * links)]
+
+    def product(x, w, y):
+        rc = N.nomas_linear_bf16(x.data_ptr(), m, x.shape[1], x.stride(0), w.data_ptr(), w.shape[0], w.stride(0), y.data_ptr(),
+                                 y.stride(0), N.NOMAS_DTYPE_BF16, status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == N.NOMAS_OK
+
+    def chain(after=lambda: None):
+        for i, y in enumerate(bufs):
+            product(x if i == 0 else bufs[i - 1], w if i % 2 == 0 else back, y)
+            after()
+
+    def overwrite():
+        for y in bufs:
+            y.fill_(float("nan"))
+        torch.cuda.synchronize()
+
+    overwrite()
+    chain(torch.cuda.synchronize)
+    expect = [y.clone() for y in bufs]
+    assert all(torch.isfinite(e).all() for e in expect)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    side = torch.cuda.Stream()
+
+    def aside():
+        with torch.cuda.stream(side):
+            chain()
+
+    for run in (chain, aside, graph.replay, graph.replay):
+        overwrite()
+        run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, e) for y, e in zip(bufs, expect))
+    assert not status.any()
