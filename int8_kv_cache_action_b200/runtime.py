@@ -348,8 +348,9 @@ class Int4Linear:
         n, k = w.shape
         codes = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
         scales = torch.empty((n, -(-k // group)), dtype=torch.bfloat16, device=w.device)
-        N._check(N.nomas_w4_quantize(w.data_ptr(), n, k, w.stride(0), group, codes.data_ptr(), scales.data_ptr(), st),
-                 "nomas_w4_quantize")
+        # a single row's own stride says nothing
+        N._check(N.nomas_w4_quantize(w.data_ptr(), n, k, w.stride(0) if n > 1 else k, group, codes.data_ptr(),
+                                     scales.data_ptr(), st), "nomas_w4_quantize")
         return cls(codes, scales, group)
 
     def dequantized(self, stream=None) -> torch.Tensor:

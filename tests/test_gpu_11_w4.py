@@ -227,3 +227,12 @@ def test_scales_near_the_largest_of_a_last_group_that_columns_end_in(m, n, k, gr
     y = lin(x, out_dtype=out_dtype)
     assert lin.status() == N.NOMAS_OK
     _check(y, x, lin)
+
+
+def test_a_single_row_of_weights_with_any_stride():
+    w = _weights(64, 1, 23).cuda().t()                         # [1, 64], strides (1, 1)
+    assert w.stride() == (1, 1)
+    lin, ref = Int4Linear.from_weights(w, 32), Int4Linear.from_weights(w.reshape(64).clone()[None], 32)
+    assert torch.equal(lin.codes, ref.codes) and torch.equal(lin.scales, ref.scales)
+    x = _acts(3, 64, 24).cuda()
+    _check(lin(x), x, lin)
