@@ -43,6 +43,11 @@ def _pitch(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
 
 
+def _split_rows(t: torch.Tensor) -> bool:
+    """Whether a matrix' rows are not contiguous; a single column's stride says nothing."""
+    return t.stride(1) != 1 and t.shape[1] != 1
+
+
 def _same_device(ref: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
     index = ref.get_device()
     for t in others:
@@ -375,7 +380,7 @@ class Int4Linear:
         m = shape[0]
         _same_device(codes, x, out)
         dtype = _DTYPES.get(out_dtype if out is None else out.dtype)
-        if dtype is None or (out is not None and (out.shape != (m, n) or out.stride(1) != 1)):
+        if dtype is None or (out is not None and (out.shape != (m, n) or _split_rows(out))):
             raise ValueError("out: bf16 or fp32 [M, N] with contiguous rows")
         if out is None:
             out, ldy = x.new_empty((m, n), dtype=out_dtype), n
@@ -487,7 +492,7 @@ class AxisRope:
 
 def _norm_params(x, weight, bias, rows_per_group):
     """(pitch, type, groups) of a layer norm's parameters: [C], or [groups, C]."""
-    if x.dim() != 2 or x.dtype not in _DTYPES or x.stride(1) != 1:
+    if x.dim() != 2 or x.dtype not in _DTYPES or _split_rows(x):
         raise ValueError("x: bf16 or fp32 [rows, C] with contiguous rows")
     rows, cols = x.shape
     if rows_per_group < 0:
@@ -502,7 +507,7 @@ def _norm_params(x, weight, bias, rows_per_group):
         shape, strides = p.shape, p.stride()
         if len(shape) == 1:
             shape, strides = (1, *shape), (cols, *strides)
-        if shape != (groups, cols) or p.dtype not in _DTYPES or strides[1] != 1:
+        if shape != (groups, cols) or p.dtype not in _DTYPES or (strides[1] != 1 and cols != 1):
             raise ValueError("weight, bias: bf16 or fp32 [groups, C] ([C] for one group) with contiguous rows")
         at = strides[0] if groups > 1 else cols
         if at < cols:
@@ -531,7 +536,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         raise ValueError("out: bf16 or fp32 [rows, C] with contiguous rows")
     if out is None:
         out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
-    elif out.shape != x.shape or out.stride(1) != 1:
+    elif out.shape != x.shape or _split_rows(out):
         raise ValueError("out: bf16 or fp32 [rows, C] with contiguous rows")
     mean = rstd = None
     if want_stats:
@@ -555,7 +560,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
             return layer_norm_backward(dy, x, mean, rstd, weight, rows_per_group, unit_offset, want_dx, want_params)
     pitch, p_dtype, groups = _norm_params(x, weight, None, rows_per_group)
     rows, cols = x.shape
-    if dy.shape != x.shape or dy.dtype not in _DTYPES or dy.stride(1) != 1:
+    if dy.shape != x.shape or dy.dtype not in _DTYPES or _split_rows(dy):
         raise ValueError("dy: bf16 or fp32 [rows, C] with contiguous rows")
     for s in (mean, rstd):
         if s.dtype != torch.float32 or s.shape != (rows,) or not s.is_contiguous():

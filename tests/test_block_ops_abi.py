@@ -96,3 +96,17 @@ def test_layernorm_parameter_rows_that_overlap_are_refused(N):
     assert _norm_params(x, views[:, 64:], views[:, :64], 2) == (128, N.NOMAS_DTYPE_BF16, 4)
     assert _norm_params(x, None, None, 2) == (64, N.NOMAS_DTYPE_F32, 4)
     assert _norm_params(x[:0], expanded[:0], None, 2)[2] == 0
+
+
+def test_a_single_column_has_contiguous_rows(N):
+    import torch
+    from int8_kv_cache_action_b200.runtime import _norm_params
+    column = torch.zeros((1, 5)).t()                          # [5, 1], contiguous, strides (1, 5)
+    assert column.is_contiguous() and column.stride(1) == 5
+    assert _norm_params(column, None, None, 0) == (1, N.NOMAS_DTYPE_F32, 1)
+    assert _norm_params(column, column[:3], column[:3], 2) == (1, N.NOMAS_DTYPE_F32, 3)
+    for bad in (torch.zeros((5, 4)).t(), torch.zeros((5, 8))[:, ::2]):
+        with pytest.raises(ValueError):
+            _norm_params(bad, None, None, 0)
+    with pytest.raises(ValueError):
+        _norm_params(column, torch.zeros(1).expand(3, 1), None, 2)

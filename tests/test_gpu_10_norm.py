@@ -246,3 +246,12 @@ def test_backward_of_a_row_whose_mean_times_rstd_overflows(cols, xt, yt):
     mean[2], rstd[2] = x[2, 0].float(), 1000.0
     _check_backward(dy, x, mean, rstd, w, 0, False)
     _check_backward(dy, x, mean, rstd, None, 2, True)
+
+
+def test_a_single_column_of_any_stride():
+    def column(seed, dtype=F32):
+        return _randn((1, 5), dtype, seed).t()                 # strides (1, 5)
+    x, w, out = column(33), column(34)[:3], torch.zeros((1, 5), device="cuda").t()
+    y, mean, rstd = _check_forward(x, w, w, 2, False, F32)
+    assert torch.equal(layer_norm(x, w, w, rows_per_group=2, out=out), y)
+    _check_backward(column(35, BF16), x, mean, rstd, w, 2, False)

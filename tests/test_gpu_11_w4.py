@@ -236,3 +236,9 @@ def test_a_single_row_of_weights_with_any_stride():
     assert torch.equal(lin.codes, ref.codes) and torch.equal(lin.scales, ref.scales)
     x = _acts(3, 64, 24).cuda()
     _check(lin(x), x, lin)
+
+
+def test_a_single_column_of_results_with_any_stride():
+    lin, x = _codes(1, 96, 32, 25), _acts(5, 96, 26).cuda()
+    out = torch.zeros((1, 5), device="cuda").t()
+    assert lin(x, out=out) is out and torch.equal(out, lin(x, out_dtype=F32))
