@@ -452,7 +452,8 @@ int nomas_layernorm_fwd(const void *x, int64_t rows, int64_t cols, int64_t ldx, 
                         const void *b, int64_t ldp, int p_dtype, int64_t rows_per_group, int unit_offset, float eps,
                         void *y, int64_t ldy, int y_dtype, float *mean, float *rstd, nomas_stream stream);
 
-/* Bytes of the backward pass' workspace on the current device: 0 on invalid arguments, else at least 16. */
+/* Bytes of the backward pass' workspace on the current device, which must be the one that holds x: devices with other
+ * numbers of SMs need other sizes.  0 on invalid arguments, else at least 16. */
 size_t nomas_layernorm_workspace_bytes(int64_t rows, int64_t cols, int64_t rows_per_group);
 
 /* mean, rstd: of the forward call.  dx, dw, db: each nullable, not all; dw, db fp32 [groups][cols], pitch

@@ -821,7 +821,7 @@ static int launch_row(const NormParams &p, cudaStream_t st) {
     return check_launch("layernorm_row_kernel launch");
 }
 
-// The row's loads spread over as many threads as a CTA has.
+// The row's loads spread over as many threads as a CTA has.  Narrow rows above 4096 columns spill about 320 bytes a thread.
 template <typename TX, typename TY, int CH>
 static int pick_row(NormParams &p, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
@@ -853,7 +853,8 @@ static int launch_fwd(NormParams &p, cudaStream_t st) {
 }
 
 // Values of a row per thread: 8 with 4 rows at a time, 16 with 2, then teams of 512 threads.  Narrow layouts hold the
-// next rows in registers and take fewer rows at a time.
+// next rows in registers and take fewer rows at a time (26400 x 3581 in bf16: 125 us, its bytes 58); above 8192 columns
+// these spill 64 to 140 bytes a thread.
 template <typename TX, typename TY, int CH>
 static int pick_fwd(NormParams &p, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;
@@ -891,8 +892,9 @@ static int any_fwd(NormParams &p, bool wide, cudaStream_t st) {
     return wide ? row_or_share<TX, TY, CH>(p, st) : row_or_share<TX, TY, 1>(p, st);
 }
 
-// Shares of the backward pass: the CTAs that the device holds at once (`per_sm` on an SM), each with at least a round
-// of rows.
+// Shares of the backward pass: `per_sm` CTAs an SM, each with at least a round of rows.  The device holds as many at once,
+// but for rows of more than 1024 columns with an fp32 side, whose ring leaves an SM one CTA of the two (13200 x 2048 in
+// fp32: 61 us, 5.3 TB/s, as in bf16).
 static void bwd_shares(int64_t rows, int64_t cols, int per_sm, int64_t *share, int64_t *ctas) {
     // small ones: a single share needs no second launch
     const int64_t most = per_sm * (int64_t)sm_count(), least = rows * cols <= 32768 ? rows : cols <= 512 ? 16 : 4;
@@ -924,7 +926,9 @@ static int launch_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
 }
 
 // Values of a row per thread: 8 with 4 rows at a time, 16 with 2, then teams of 512 threads.  Narrow layouts hold the
-// next rows in registers and take half as many values.
+// next rows in registers and take half as many values.  Above 8192 columns a thread's 32 values of u + w, x, dy, dw and db
+// do not fit 128 registers and spill, 0.5 to 0.6 KB a thread with a ring and up to 2.7 without: 1000 x 16384 takes 51 us in
+// bf16 (its bytes 15) and 161 in fp32 (30).
 template <typename TX, typename TY, int CH>
 static int pick_bwd(NormBwdParams &p, int64_t ctas, cudaStream_t st) {
     const int64_t chunks = (p.cols + CH - 1) / CH;

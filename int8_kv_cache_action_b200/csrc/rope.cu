@@ -22,7 +22,8 @@ constexpr int kRopeMaxPairs = NOMAS_ROPE_MAX_HEAD_DIM / 2;
 // How a pair's values are reached: in one 16-byte chunk (interleaved), in two chunks that the same thread holds (halves,
 // where every axis' half is whole chunks of 16, or in bf16 of 8 bytes), or one by one (halves of other widths:
 // rope_pairs_kernel).  26400 tokens of 2 x 16 x 128 in bf16, halves: chunks of 16 bytes (axes 32, 48, 48) 83 us, of 8
-// (16, 56, 56) 76, one by one (44, 42, 42) 111, which is also what 16, 56, 56 took one by one.
+// (16, 56, 56) 76, one by one (44, 42, 42) 111, which is also what 16, 56, 56 took one by one.  The rule goes by alignment;
+// the chunks of 16 bytes with two items a thread spill 28 to 32 bytes a thread, those of 8 none.
 enum RopeForm { kRopeInside = 0, kRopeTwoChunks = 1, kRopePairs = 2 };
 
 struct RopeTensor {

@@ -76,8 +76,10 @@ struct W4Codes {
     __nv_bfloat16 f[RT][2];
 };
 
-// CTAs of an SM, from the warps that the sums of RT * NT products leave registers for.  24 warps spill a little with
-// RT = 2, and pay on wide matrices (2 x 8192 -> 28001: 35.6 us, 43.9 with 20, 45.3 with 16).
+// CTAs of an SM, from the warps that the sums of RT * NT products leave registers for.  24 warps spill 52 to 116 bytes a
+// thread with RT = 2, and pay on wide matrices (2 x 8192 -> 28001: 35.6 us, 43.9 with 20, 45.3 with 16).  The 16 warps of
+// more rows of x spill too: 32 and 40 bytes with <2, 2>, 268 and 276 with <4, 2> (30 x 2048 -> 12288, 13.5 us where its
+// bytes take 2.2), 8 to 32 with <4, 1>.
 template <int NT, int RT, int WARPS>
 constexpr int w4_ctas = (NT * RT <= 2 ? 24 : 16) / WARPS > 0 ? (NT * RT <= 2 ? 24 : 16) / WARPS : 1;
 
@@ -223,8 +225,11 @@ __global__ void __launch_bounds__(32 * WARPS, w4_ctas<NT, RT, WARPS>) w4_rows_ke
 // widen.  A ninth warp issues copies and products (issued by a widening warp, that warp held up the others: 1850 cycles
 // a half slab instead of 700).  The tensor core truncates its sums, so the sums of every 512 columns leave TMEM for fp32
 // additions in registers.  Two buffers of A and x, and two CTAs an SM, hide each other's waits.  At the end the CTAs of
-// a cluster add their sums up through distributed shared memory, in rank order.  Bound by the tensor core's reading of A
-// from TMEM, 64 cycles and more for 16 columns whatever the rows of x, so it pays from about 17 of them on.
+// a cluster add their sums up through distributed shared memory, in rank order.
+// A slab takes as long whatever the rows of x (8192 -> 28001: 2 rows 75 us, 16 rows 78, against 34 and 54 by
+// w4_rows_kernel), so it pays from about 17 of them on.  64 x 8192 -> 8192: 33 us, where its bytes take 5.8.  No unit is
+// near its limit there (tensor pipe 13 % busy, DRAM 12 %, half the issue slots): what is left is most likely the latency
+// of a half slab's chain, from x to the product's commit, which two buffers and two CTAs an SM hide in part.
 constexpr int kTileRows = 128, kSlab = 256, kTileThreads = 256;        // threads that widen; one more warp issues
 constexpr uint32_t kTileTmem = 256, kTileD = 128;      // TMEM columns of a CTA: A at 0, D at kTileD
 constexpr int kTileStage = kTileRows * kSlab / 2;
@@ -631,7 +636,7 @@ static int enqueue_w4_sums(const void *x, int64_t m, int64_t k_in, int64_t ldx, 
 
 // Rows of x that need no GEMM: up to 128 of them the widened weights' way through memory costs more than it saves where
 // rows are long, or W small (us, GEMM with its dequantise pass against this file's kernels: 128 x 2048 -> 2048 13 / 12,
-// x 4096 -> 4096 23 / 25, x 8192 -> 2048 36 / 23, x 8192 -> 8192 65 / 57, x 2048 -> 12288 21 / 36).
+// x 4096 -> 4096 23 / 24, where the two sides meet, x 8192 -> 2048 36 / 23, x 8192 -> 8192 65 / 57, x 2048 -> 12288 21 / 36).
 static bool w4_few(int64_t m, int64_t n_out, int64_t k_in) {
     if (m <= NOMAS_W4_FEW_ROWS || (m <= 128 && (n_out <= 4096 || k_in >= 4096))) return true;
     // products that take less than the GEMM's launches (some 20 us)
@@ -692,8 +697,9 @@ static int pick_w4_rows(const W4Params &p, cudaStream_t st) {
 }
 
 // Whether few rows of x go to w4_tile_kernel rather than w4_rows_kernel, which takes 32 of them at a time and has less
-// to set up (us, rows against tiles: 64 x 8192 -> 8192 64 / 32, x 2048 -> 12288 28 / 20, x 4096 -> 4096 19 / 15,
-// x 2048 -> 2048 8 / 11; 30 x 8192 -> 8192 32 / 25, x 2048 -> 12288 14 / 17; 128 x 2048 -> 2048 15 / 12).
+// to set up (us, rows against tiles: 64 x 8192 -> 8192 64 / 33, x 2048 -> 12288 28 / 20, x 4096 -> 4096 19 / 15,
+// x 2048 -> 2048 8 / 11; 30 x 8192 -> 8192 32 / 26, x 2048 -> 12288 14 / 16, x 4096 -> 4096 12 / 12; 16 x 8192 -> 8192
+// 19 / 25; 128 x 2048 -> 2048 15 / 11).
 static bool w4_tiles(int64_t m, int64_t n_out, int64_t k_in) {
     const int64_t weights = n_out * k_in;
     return m > 64 ? weights >= 1 << 22 : m > 32 ? weights >= 1 << 23 : m > 16 && weights >= 1 << 26;

@@ -5,6 +5,10 @@ modulation (layer_norm, layer_norm_backward) and the linear layers with INT8 and
 
 Only allocation (torch), stream selection and argument marshalling happen here; the quantise-append,
 mask build, attention and these operators all run in libnomas's kernels.
+
+No call records an autograd graph, whatever its inputs require: results carry no gradient function, and a
+tensor written through out= keeps its version.  Gradients are calls of their own: layer_norm_backward, and
+AxisRope with inverse=True.
 """
 from __future__ import annotations
 
@@ -523,7 +527,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
                out: Optional[torch.Tensor] = None, want_stats: bool = False, stream=None):
     """Layer norm of the rows of x [rows, C] (include/nomas.h): xhat * weight + bias, or with unit_offset
     xhat * (1 + weight) + bias (modulation).  rows_per_group: rows that share a row of weight and bias
-    ([groups, C]); 0: one weight and bias [C] for all.  Returns y, or (y, mean, rstd) with want_stats, which
+    ([groups, C], every row its own memory, so no expanded one); 0: one weight and bias [C] for all.  Returns y, or (y, mean, rstd) with want_stats, which
     layer_norm_backward takes."""
     st = _stream_on(x, stream)
     if st is None:
